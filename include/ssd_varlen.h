@@ -85,6 +85,7 @@ enum ssd_status {
 #define SSD_DEVERR_BLOCK_TABLE 0x20  /* a boundary needs a column >= block_table_width */
 #define SSD_DEVERR_TIMEOUT 0x40      /* a bounded wait inside a kernel gave up (work skipped) */
 #define SSD_DEVERR_INTERNAL 0x80     /* a kernel could not start (shared-memory alignment) */
+#define SSD_DEVERR_TOKEN 0x200       /* ssd_varlen_verify: a drafted token outside [0, V) (rejected) */
 #define SSD_DEVERR_ALIAS 0x100       /* ssd_varlen_check_slots: a written slot is read or written twice */
 
 /* Problem sizes.  Filled by the caller, copied into the plan. */
@@ -386,6 +387,194 @@ typedef struct ssd_gdn_io {
 
 int ssd_varlen_gdn_forward(const ssd_gdn_dims *dims, const int32_t *cu_seqlens, const ssd_gdn_io *io,
                            cudaStream_t stream);
+
+/* ---- Selective scan (S6) prefill --------------------------------------------
+ * The scan of a selective state space layer whose step is per channel and whose
+ * decay is per channel and state ("Mamba: Linear-Time Sequence Modeling with
+ * Selective State Spaces", section 3), over the packed varlen batch of the
+ * forward above.  For request i, channel d with group g = d / (D/G), state n,
+ * token by token:
+ *     dt'    = softplus(delta[t,d] + delta_bias[d])     (dims.softplus != 0)
+ *              delta[t,d] + delta_bias[d]               (dims.softplus == 0)
+ *     h[d,n] <- exp(dt' A[d,n]) h[d,n] + dt' u[t,d] B[t,g,n]
+ *     y[t,d] = (sum_n C[t,g,n] h[d,n] + D[d] u[t,d]) * silu(z[t,d])
+ * u is the output of the layer's causal conv1d (ssd_varlen_conv1d for prompts,
+ * ssd_varlen_conv1d_step for windows): delta, B and C are projections of it, so
+ * the convolution is a call of its own.
+ *
+ * The state starts from state_pool[init_slots[i]] (zeros when < 0 or NULL); the
+ * final state goes to final_states[i] and state_pool[final_slots[i]], and the
+ * state after every absolute multiple kb of block_size in (s, s+L], with s =
+ * num_computed[i], to state_pool[block_table[i*block_table_width +
+ * kb/block_size - 1]] (entries < 0 skipped): the forward's rules.  An empty
+ * request's final state is its initial state.  Write slots must not alias read
+ * slots of the same call.
+ *
+ * Layouts: u, delta, z, y (T,D) and B, C (T,G,N) in dims.dtype, with a distance
+ * between the rows of two tokens that each tensor has for itself (the *_stride
+ * fields, in elements; 0 = contiguous), so slices of the projections' outputs
+ * are taken as they are; a row is contiguous.  A (D,N), D (D), delta_bias (D)
+ * and the states (..., D, N) fp32, contiguous.  Pointers need the alignment of
+ * their elements only; rows that all start on 16-byte boundaries are read
+ * faster.  1 <= N <= 256; D a multiple of G; block_size a multiple of 16 where
+ * a block_table is given.  y must not overlap an input.
+ *
+ * delta, A and the inputs are taken as they are: a NaN or an infinity reaches
+ * the y and the state of its own channel (its own group for B and C) from its
+ * token on, and no other request.
+ *
+ * Host-visible violations return SSD_ERR_* before any launch; device_err (one
+ * int32 in device memory, required) receives SSD_DEVERR_* bits (CU_SEQLENS,
+ * NUM_COMPUTED, INIT_SLOT, FINAL_SLOT, BLOCK_SLOT, BLOCK_TABLE; NUM_COMPUTED
+ * only where a block_table is given); a bad read is zeros, a bad write is
+ * skipped.  With T = 0 the token buffers may be NULL.
+ * `workspace` (16-byte aligned, at least ssd_varlen_selective_scan_workspace
+ * bytes; NULL where that is 0) is scratch: it holds nothing between calls.
+ * Launches only on `stream`; allocates nothing; can be captured into a graph. */
+typedef struct ssd_selective_dims {
+    int64_t T;                 /* total tokens, >= 0 */
+    int32_t R;                 /* requests, >= 1 */
+    int32_t D, N, G;           /* channels, states a channel, groups of B and C (D % G == 0) */
+    int32_t dtype;             /* enum ssd_dtype of u, delta, B, C, z, y */
+    int32_t num_slots;         /* rows of state_pool (0 when no pool is used) */
+    int32_t block_size;        /* block-checkpoint granularity; 0 = none */
+    int32_t block_table_width; /* columns of block_table */
+    int32_t softplus;          /* 1: dt' = softplus(delta + bias), 0: delta + bias */
+    int32_t reserved;          /* must be 0 */
+    int64_t u_stride, delta_stride, B_stride, C_stride, z_stride, y_stride; /* elements; 0 = contiguous */
+} ssd_selective_dims;
+
+typedef struct ssd_selective_io {
+    const void *u, *delta;       /* (T,D) */
+    const float *delta_bias;     /* (D) or NULL */
+    const float *A;              /* (D,N) */
+    const void *B, *C;           /* (T,G,N) */
+    const float *D;              /* (D) or NULL: no skip term */
+    const void *z;               /* (T,D) or NULL: no gate */
+    const int32_t *num_computed; /* (R) tokens already in each request's state, or NULL */
+    float *state_pool;           /* (num_slots,D,N) or NULL */
+    const int32_t *init_slots;   /* (R) or NULL */
+    const int32_t *final_slots;  /* (R) or NULL */
+    const int32_t *block_table;  /* (R, block_table_width) or NULL; needs block_size > 0 */
+    void *y;                     /* (T,D) */
+    float *final_states;         /* (R,D,N) or NULL */
+    void *workspace;             /* scratch, or NULL where none is needed */
+    size_t workspace_bytes;
+    int32_t *device_err;         /* one int32, OR-ed with SSD_DEVERR_* bits */
+} ssd_selective_io;
+
+/* Bytes of scratch that ssd_varlen_selective_scan needs for these dims (0: none). */
+size_t ssd_varlen_selective_scan_workspace(const ssd_selective_dims *dims);
+
+int ssd_varlen_selective_scan(const ssd_selective_dims *dims, const int32_t *cu_seqlens,
+                              const ssd_selective_io *io, cudaStream_t stream);
+
+/* ---- Selective-scan step for decode and speculative windows ------------------
+ * The same recurrence over short per-request windows with the anchors of
+ * ssd_varlen_decode: request i's tokens [cu_seqlens[i], cu_seqlens[i+1]) start
+ * from state_pool[read_slots[i]] (zeros when < 0) and the state after token t
+ * goes to state_pool[write_slots[t]] when that slot is >= 0, so the step after
+ * verification can read the state after the last accepted token.  An empty
+ * window reads and writes nothing.  dims as above (block_size and
+ * block_table_width are not used; num_slots >= 1); write_slots (T) is nullable,
+ * as are z, D and delta_bias.  A write slot must not be a slot read in the same
+ * call.  device_err receives CU_SEQLENS, INIT_SLOT (a read slot >= num_slots:
+ * read as zeros), FINAL_SLOT (a write slot >= num_slots: skipped).  One launch
+ * on `stream`; allocates nothing. */
+typedef struct ssd_selective_step_io {
+    const void *u, *delta;      /* (T,D) */
+    const float *delta_bias;    /* (D) or NULL */
+    const float *A;             /* (D,N) */
+    const void *B, *C;          /* (T,G,N) */
+    const float *D;             /* (D) or NULL */
+    const void *z;              /* (T,D) or NULL */
+    float *state_pool;          /* (num_slots,D,N) fp32, read and written */
+    const int32_t *read_slots;  /* (R), < 0 = zero state */
+    const int32_t *write_slots; /* (T), < 0 = none; or NULL */
+    void *y;                    /* (T,D) */
+    int32_t *device_err;        /* one int32, OR-ed with SSD_DEVERR_* bits */
+} ssd_selective_step_io;
+
+int ssd_varlen_selective_step(const ssd_selective_dims *dims, const int32_t *cu_seqlens,
+                              const ssd_selective_step_io *io, cudaStream_t stream);
+
+/* ---- Causal conv1d step for decode and speculative windows -------------------
+ * ssd_varlen_conv1d over short per-request windows, with a write anchor for
+ * every token instead of one for every request: io->write_slots is (T) here, and
+ * the conv state after token t (its own input and the W-2 before it, oldest
+ * first, bit for bit) goes to conv_pool[write_slots[t]] when that slot is >= 0.
+ * io->read_slots is (R) and may be NULL (every window starts from zeros).  An
+ * empty window reads and writes nothing.  dims and io as for ssd_varlen_conv1d,
+ * with any D >= 1 and pointers aligned to their elements (16-byte aligned x, y
+ * and pool with D a multiple of 16 bytes are read faster); sums and the SiLU are
+ * fp32.  device_err receives CU_SEQLENS, INIT_SLOT, FINAL_SLOT.  One launch on
+ * `stream`; allocates nothing. */
+int ssd_varlen_conv1d_step(const ssd_conv_dims *dims, const int32_t *cu_seqlens, const ssd_conv_io *io,
+                           cudaStream_t stream);
+
+/* ---- Verification of drafted tokens --------------------------------------------
+ * Speculative sampling ("Accelerating Large Language Model Decoding with
+ * Speculative Sampling", algorithm 2) over the windows of ssd_varlen_decode and
+ * ssd_varlen_selective_step, from given random numbers.  Window i is the packed
+ * rows [a, b) = [cu_seqlens[i], cu_seqlens[i+1]): tokens[a] is the request's last
+ * token, tokens[a+1 .. b-1] its k = b-a-1 drafts; target[t] is the target
+ * model's distribution of the token after t, draft[t] the one that tokens[t+1]
+ * was drawn from (the last row of a window is not read), NULL for drafts that
+ * have no distribution (n-gram, greedy drafts): then draft[t] is 1 at the drafted
+ * token and 0 elsewhere.
+ *   For t = a, a+1, ...: the draft x = tokens[t+1] is accepted when
+ *       accept_u[t+1] * draft[t][x] < target[t][x]      (fp32)
+ *   and the first that is not ends it; n drafts are accepted, and row r = a + n
+ *   gives the token that follows them, from the weights
+ *       w_v = target[r][v] - draft[r][v]   after a rejection (n < k)
+ *       w_v = target[r][v]                 when every draft was accepted
+ *   (target[r] too where no w_v is positive after a rejection).
+ * The token is drawn by inversion in the order of the vocabulary, with weights
+ * held as whole multiples of 2^-40: f_v = floor(2^40 min(max(w_v, 0), 1)), 0 for
+ * a NaN; S = sum of f_v; the token is the first v with f_0 + ... + f_v >
+ * min(floor(sample_u[i] S), S - 1), the product in fp64.  Sums of whole numbers
+ * have no order, so the result is the same bit for bit whatever the split.  A
+ * row without a positive weight gives the token -1.  accept_u and sample_u are
+ * uniform in [0, 1); below 0 or NaN sample_u counts as 0.
+ *
+ * Outputs: accepted[i] = n (-1 for an empty window); out_tokens (T): the n
+ * accepted drafts from row a on, the drawn token at row a + n, -1 after it;
+ * next_slots[i] = write_slots[a + n]: the slot that holds the state after the
+ * last accepted token, i.e. the read anchor of the request's next step.  An
+ * empty window leaves next_slots[i] as it is.  write_slots and next_slots are
+ * given together or are both NULL; next_slots may be the read_slots array of
+ * the step before (on the same stream).
+ *
+ * target, draft (T,V) in dims.dtype with a distance between rows of their own
+ * (elements; 0 = V); pointers aligned to their elements (16-byte aligned rows
+ * are read faster).  A drafted token outside [0, V) is rejected and sets
+ * SSD_DEVERR_TOKEN; windows that cu_seqlens orders wrongly set CU_SEQLENS and
+ * are skipped.  With T = 0 the token buffers may be NULL.  One launch on
+ * `stream`; allocates nothing. */
+typedef struct ssd_verify_dims {
+    int64_t T;                            /* rows of all windows, >= 0 */
+    int32_t R;                            /* windows, >= 1 */
+    int32_t V;                            /* vocabulary, 1 .. 2^22 */
+    int32_t dtype;                        /* enum ssd_dtype of target and draft */
+    int32_t reserved;                     /* must be 0 */
+    int64_t target_stride, draft_stride;  /* elements between rows; 0 = V */
+} ssd_verify_dims;
+
+typedef struct ssd_verify_io {
+    const void *target;         /* (T,V) probabilities */
+    const void *draft;          /* (T,V) probabilities, or NULL */
+    const int32_t *tokens;      /* (T) */
+    const float *accept_u;      /* (T) */
+    const float *sample_u;      /* (R) */
+    const int32_t *write_slots; /* (T) the step's write anchors, or NULL */
+    int32_t *accepted;          /* (R) */
+    int32_t *out_tokens;        /* (T) */
+    int32_t *next_slots;        /* (R), or NULL */
+    int32_t *device_err;        /* one int32, OR-ed with SSD_DEVERR_* bits */
+} ssd_verify_io;
+
+int ssd_varlen_verify(const ssd_verify_dims *dims, const int32_t *cu_seqlens, const ssd_verify_io *io,
+                      cudaStream_t stream);
 
 /* ---- Slot aliasing check (for debug runs) ------------------------------------
  * The calls above require that no pool slot written in a call is also read in

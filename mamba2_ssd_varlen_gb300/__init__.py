@@ -19,6 +19,11 @@ The functions keep the C names:
   ssd_varlen_align_bite(start, end, total, align) (block-aligned prefill bite, host)
   ssd_varlen_gdn_forward(dims, cu_seqlens, io)   (gated delta rule prefill by chunks)
   ssd_varlen_check_slots(dims, init, final, block_table, err)  (slot-aliasing check, debug)
+  ssd_varlen_selective_scan_workspace(dims)      -> bytes
+  ssd_varlen_selective_scan(dims, cu_seqlens, io) (selective-scan (S6) prefill)
+  ssd_varlen_selective_step(dims, cu_seqlens, io) (its decode / speculative-window step)
+  ssd_varlen_conv1d_step(dims, cu_seqlens, io)   (causal conv1d of such windows, a state slot per token)
+  ssd_varlen_verify(dims, cu_seqlens, io)        (drafted tokens against the target's probabilities)
 and ``run(...)`` wires a whole call from torch tensors (tests and bench use it).
 """
 from __future__ import annotations
@@ -34,7 +39,7 @@ DTYPE_F32 = 1
 
 DEVERR = {
     "CU_SEQLENS": 0x1, "NUM_COMPUTED": 0x2, "INIT_SLOT": 0x4, "FINAL_SLOT": 0x8,
-    "BLOCK_SLOT": 0x10, "BLOCK_TABLE": 0x20, "TIMEOUT": 0x40, "INTERNAL": 0x80, "ALIAS": 0x100,
+    "BLOCK_SLOT": 0x10, "BLOCK_TABLE": 0x20, "TIMEOUT": 0x40, "INTERNAL": 0x80, "ALIAS": 0x100, "TOKEN": 0x200,
 }
 STATUS = {
     0: "OK", -1: "NULL", -2: "DIMS", -3: "CHUNK_SIZE", -4: "GROUPS", -5: "BLOCK_SIZE",
@@ -44,7 +49,8 @@ EXPORTED = ["ssd_varlen_workspace_size", "ssd_varlen_count_chunks", "ssd_varlen_
             "ssd_varlen_forward", "ssd_varlen_status", "ssd_varlen_strerror",
             "ssd_varlen_forward_static", "ssd_varlen_decode", "ssd_varlen_conv1d",
             "ssd_varlen_align_bite", "ssd_varlen_gdn_forward", "ssd_varlen_check_slots",
-            "ssd_varlen_forward_path"]
+            "ssd_varlen_forward_path", "ssd_varlen_selective_scan_workspace", "ssd_varlen_selective_scan",
+            "ssd_varlen_selective_step", "ssd_varlen_conv1d_step", "ssd_varlen_verify"]
 # enum ssd_path
 PATH_TENSOR_CORE = 1
 PATH_GENERAL = 2
@@ -108,6 +114,37 @@ class ssd_gdn_io(ctypes.Structure):
                 ("o", c_vp), ("final_states", c_vp), ("chunk_states", c_vp), ("device_err", c_vp)]
 
 
+class ssd_selective_dims(ctypes.Structure):
+    _fields_ = [("T", c_i64), ("R", c_i32), ("D", c_i32), ("N", c_i32), ("G", c_i32), ("dtype", c_i32),
+                ("num_slots", c_i32), ("block_size", c_i32), ("block_table_width", c_i32), ("softplus", c_i32),
+                ("reserved", c_i32), ("u_stride", c_i64), ("delta_stride", c_i64), ("B_stride", c_i64),
+                ("C_stride", c_i64), ("z_stride", c_i64), ("y_stride", c_i64)]
+
+
+class ssd_selective_io(ctypes.Structure):
+    _fields_ = [("u", c_vp), ("delta", c_vp), ("delta_bias", c_vp), ("A", c_vp), ("B", c_vp), ("C", c_vp),
+                ("D", c_vp), ("z", c_vp), ("num_computed", c_vp), ("state_pool", c_vp), ("init_slots", c_vp),
+                ("final_slots", c_vp), ("block_table", c_vp), ("y", c_vp), ("final_states", c_vp),
+                ("workspace", c_vp), ("workspace_bytes", ctypes.c_size_t), ("device_err", c_vp)]
+
+
+class ssd_selective_step_io(ctypes.Structure):
+    _fields_ = [("u", c_vp), ("delta", c_vp), ("delta_bias", c_vp), ("A", c_vp), ("B", c_vp), ("C", c_vp),
+                ("D", c_vp), ("z", c_vp), ("state_pool", c_vp), ("read_slots", c_vp), ("write_slots", c_vp),
+                ("y", c_vp), ("device_err", c_vp)]
+
+
+class ssd_verify_dims(ctypes.Structure):
+    _fields_ = [("T", c_i64), ("R", c_i32), ("V", c_i32), ("dtype", c_i32), ("reserved", c_i32),
+                ("target_stride", c_i64), ("draft_stride", c_i64)]
+
+
+class ssd_verify_io(ctypes.Structure):
+    _fields_ = [("target", c_vp), ("draft", c_vp), ("tokens", c_vp), ("accept_u", c_vp), ("sample_u", c_vp),
+                ("write_slots", c_vp), ("accepted", c_vp), ("out_tokens", c_vp), ("next_slots", c_vp),
+                ("device_err", c_vp)]
+
+
 class SsdError(RuntimeError):
     def __init__(self, code, what):
         super().__init__(f"{what}: {STATUS.get(code, code)} ({ssd_varlen_strerror(code)})")
@@ -158,6 +195,18 @@ def load_library():
                                             ctypes.POINTER(ssd_outputs), ctypes.POINTER(ctypes.c_int),
                                             ctypes.POINTER(ctypes.c_int)]
     lib.ssd_varlen_forward_path.restype = ctypes.c_int
+    lib.ssd_varlen_selective_scan_workspace.argtypes = [ctypes.POINTER(ssd_selective_dims)]
+    lib.ssd_varlen_selective_scan_workspace.restype = ctypes.c_size_t
+    lib.ssd_varlen_selective_scan.argtypes = [ctypes.POINTER(ssd_selective_dims), c_vp,
+                                              ctypes.POINTER(ssd_selective_io), c_vp]
+    lib.ssd_varlen_selective_scan.restype = ctypes.c_int
+    lib.ssd_varlen_selective_step.argtypes = [ctypes.POINTER(ssd_selective_dims), c_vp,
+                                              ctypes.POINTER(ssd_selective_step_io), c_vp]
+    lib.ssd_varlen_selective_step.restype = ctypes.c_int
+    lib.ssd_varlen_conv1d_step.argtypes = [ctypes.POINTER(ssd_conv_dims), c_vp, ctypes.POINTER(ssd_conv_io), c_vp]
+    lib.ssd_varlen_conv1d_step.restype = ctypes.c_int
+    lib.ssd_varlen_verify.argtypes = [ctypes.POINTER(ssd_verify_dims), c_vp, ctypes.POINTER(ssd_verify_io), c_vp]
+    lib.ssd_varlen_verify.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -486,3 +535,216 @@ def ssd_varlen_check_slots(R, init_slots=None, final_slots=None, block_table=Non
         raise SsdError(rc, "ssd_varlen_check_slots")
     torch.cuda.synchronize(dev)
     return int(err[0].item())
+
+
+def ssd_varlen_selective_scan_workspace(dims: ssd_selective_dims) -> int:
+    return int(load_library().ssd_varlen_selective_scan_workspace(ctypes.byref(dims)))
+
+
+def ssd_varlen_selective_scan(dims: ssd_selective_dims, cu_seqlens, io: ssd_selective_io, stream=None):
+    rc = load_library().ssd_varlen_selective_scan(ctypes.byref(dims), _ptr(cu_seqlens), ctypes.byref(io),
+                                                  _stream(stream))
+    if rc != 0:
+        raise SsdError(rc, "ssd_varlen_selective_scan")
+
+
+def ssd_varlen_selective_step(dims: ssd_selective_dims, cu_seqlens, io: ssd_selective_step_io, stream=None):
+    rc = load_library().ssd_varlen_selective_step(ctypes.byref(dims), _ptr(cu_seqlens), ctypes.byref(io),
+                                                  _stream(stream))
+    if rc != 0:
+        raise SsdError(rc, "ssd_varlen_selective_step")
+
+
+def ssd_varlen_conv1d_step(dims: ssd_conv_dims, cu_seqlens, io: ssd_conv_io, stream=None):
+    rc = load_library().ssd_varlen_conv1d_step(ctypes.byref(dims), _ptr(cu_seqlens), ctypes.byref(io),
+                                               _stream(stream))
+    if rc != 0:
+        raise SsdError(rc, "ssd_varlen_conv1d_step")
+
+
+def ssd_varlen_verify(dims: ssd_verify_dims, cu_seqlens, io: ssd_verify_io, stream=None):
+    rc = load_library().ssd_varlen_verify(ctypes.byref(dims), _ptr(cu_seqlens), ctypes.byref(io), _stream(stream))
+    if rc != 0:
+        raise SsdError(rc, "ssd_varlen_verify")
+
+
+def _row_stride(t, row_shape, dtype, what):
+    """Elements between the rows of t (tokens first), whose rows must be contiguous and of row_shape; 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or tuple(t.shape[1:]) != tuple(row_shape):
+        raise ValueError(f"{what}: {t.dtype} {tuple(t.shape)}, expected {dtype} (T, {', '.join(map(str, row_shape))})")
+    n = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != n:
+            raise ValueError(f"{what}: a token's row must be contiguous")
+        n *= size
+    if t.shape[0] > 1 and t.stride(0) < n:
+        raise ValueError(f"{what}: token rows overlap (stride {t.stride(0)})")
+    return int(t.stride(0)) if t.shape[0] > 1 else n
+
+
+def _check_plain(t, shape, dtype, what):
+    """t (or None) is contiguous, of this shape and type."""
+    if t is None:
+        return
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what}: {t.dtype} {tuple(t.shape)}, expected a contiguous {dtype} {tuple(shape)}")
+
+
+def _selective_dims(prob, num_slots, block_size=0, block_table_width=0):
+    import torch
+    u, A = prob["u"], prob["A"]
+    if u.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"u: {u.dtype}, expected torch.bfloat16 or torch.float32")
+    D, N = A.shape
+    G = prob["B"].shape[1]
+    row = lambda name, shape: _row_stride(prob.get(name), shape, u.dtype, name)  # noqa: E731
+    T = u.shape[0]
+    for name in ("delta", "B", "C", "z"):
+        t = prob.get(name)
+        if t is not None and t.shape[0] != T:
+            raise ValueError(f"{name}: {t.shape[0]} tokens, expected {T}")
+    _check_plain(A, (D, N), torch.float32, "A")
+    _check_plain(prob.get("D"), (D,), torch.float32, "D")
+    _check_plain(prob.get("delta_bias"), (D,), torch.float32, "delta_bias")
+    return ssd_selective_dims(T, prob["cu_seqlens"].shape[0] - 1, D, N, G,
+                              DTYPE_F32 if u.dtype == torch.float32 else DTYPE_BF16, num_slots, block_size,
+                              block_table_width, 1 if prob.get("softplus") else 0, 0, row("u", (D,)),
+                              row("delta", (D,)), row("B", (G, N)), row("C", (G, N)), row("z", (D,)), 0)
+
+
+class SelectiveScanCall:
+    """One selective-scan prefill over a problem from workloads.make_selective_problem: outputs (y,
+    final_states), the device error word, the workspace, and the pre-built argument structs."""
+
+    def __init__(self, prob: dict, stream=None):
+        import torch
+        self.prob = prob
+        u = prob["u"]
+        pool, bt = prob.get("state_pool"), prob.get("block_table")
+        self.dims = _selective_dims(prob, 0 if pool is None else pool.shape[0], int(prob.get("block_size") or 0),
+                                    0 if bt is None else bt.shape[1])
+        R, D, N = self.dims.R, self.dims.D, self.dims.N
+        _check_plain(pool, (self.dims.num_slots, D, N), torch.float32, "state_pool")
+        self.y = torch.empty(u.shape, dtype=u.dtype, device=u.device)
+        self.final_states = (torch.empty((R, D, N), dtype=torch.float32, device=u.device)
+                             if prob.get("final_dense", True) else None)
+        self.err = torch.zeros(4, dtype=torch.int32, device=u.device)
+        need = ssd_varlen_selective_scan_workspace(self.dims)
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=u.device) if need else None
+        self.io = ssd_selective_io(_ptr(u), _ptr(prob["delta"]), _ptr(prob.get("delta_bias")), _ptr(prob["A"]),
+                                   _ptr(prob["B"]), _ptr(prob["C"]), _ptr(prob.get("D")), _ptr(prob.get("z")),
+                                   _ptr(prob.get("num_computed")), _ptr(pool), _ptr(prob.get("init_slots")),
+                                   _ptr(prob.get("final_slots")), _ptr(bt), _ptr(self.y), _ptr(self.final_states),
+                                   _ptr(self.workspace), need, _ptr(self.err))
+        self.stream = stream
+
+    def __call__(self):
+        ssd_varlen_selective_scan(self.dims, self.prob["cu_seqlens"], self.io, self.stream)
+        return self
+
+    def status(self) -> int:
+        """Device error bits of the calls so far (synchronises), then clears them."""
+        v = int(self.err[0].item())
+        self.err.zero_()
+        return v
+
+
+def run_selective_scan(prob: dict, **kw) -> SelectiveScanCall:
+    """One selective-scan prefill on the current stream; returns the SelectiveScanCall (outputs on it)."""
+    return SelectiveScanCall(prob, **kw)()
+
+
+class SelectiveStepCall:
+    """One selective-scan step over decode or speculative windows (workloads.make_selective_step_problem):
+    the output y, the device error word, and the pre-built argument structs; the pool is updated."""
+
+    def __init__(self, prob: dict, stream=None):
+        import torch
+        self.prob = prob
+        u, pool = prob["u"], prob["state_pool"]
+        self.dims = _selective_dims(prob, pool.shape[0])
+        _check_plain(pool, (pool.shape[0], self.dims.D, self.dims.N), torch.float32, "state_pool")
+        self.y = torch.empty(u.shape, dtype=u.dtype, device=u.device)
+        self.err = torch.zeros(4, dtype=torch.int32, device=u.device)
+        self.io = ssd_selective_step_io(_ptr(u), _ptr(prob["delta"]), _ptr(prob.get("delta_bias")), _ptr(prob["A"]),
+                                        _ptr(prob["B"]), _ptr(prob["C"]), _ptr(prob.get("D")), _ptr(prob.get("z")),
+                                        _ptr(pool), _ptr(prob["read_slots"]), _ptr(prob.get("write_slots")),
+                                        _ptr(self.y), _ptr(self.err))
+        self.stream = stream
+
+    def __call__(self):
+        ssd_varlen_selective_step(self.dims, self.prob["cu_seqlens"], self.io, self.stream)
+        return self
+
+    def status(self) -> int:
+        v = int(self.err[0].item())
+        self.err.zero_()
+        return v
+
+
+def run_selective_step(prob: dict, **kw) -> SelectiveStepCall:
+    """One selective-scan step on the current stream; returns the SelectiveStepCall (y on it, pool updated)."""
+    return SelectiveStepCall(prob, **kw)()
+
+
+class ConvStepCall(Conv1dCall):
+    """One causal conv1d step over decode or speculative windows: a Conv1dCall whose write_slots has a slot
+    for every token (and whose D may be any)."""
+
+    def __call__(self):
+        ssd_varlen_conv1d_step(self.dims, self.prob["cu_seqlens"], self.io, self.stream)
+        return self
+
+
+def run_conv1d_step(prob: dict, **kw) -> ConvStepCall:
+    """One conv1d step on the current stream; returns the ConvStepCall (y on it, conv states updated)."""
+    return ConvStepCall(prob, **kw)()
+
+
+class VerifyCall:
+    """One verification of drafted tokens (workloads.make_verify_problem): outputs (accepted, out_tokens,
+    next_slots where write_slots is given), the device error word, and the pre-built argument structs."""
+
+    def __init__(self, prob: dict, stream=None):
+        import torch
+        self.prob = prob
+        p, q = prob["target"], prob.get("draft")
+        T, V = p.shape
+        R = prob["cu_seqlens"].shape[0] - 1
+        if p.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"target: {p.dtype}, expected torch.bfloat16 or torch.float32")
+        if q is not None and q.shape[0] != T:
+            raise ValueError(f"draft: {q.shape[0]} rows, expected {T}")
+        slots = prob.get("write_slots")
+        _check_plain(prob["tokens"], (T,), torch.int32, "tokens")
+        _check_plain(prob["accept_u"], (T,), torch.float32, "accept_u")
+        _check_plain(prob["sample_u"], (R,), torch.float32, "sample_u")
+        _check_plain(slots, (T,), torch.int32, "write_slots")
+        self.dims = ssd_verify_dims(T, R, V, DTYPE_F32 if p.dtype == torch.float32 else DTYPE_BF16, 0,
+                                    _row_stride(p, (V,), p.dtype, "target"), _row_stride(q, (V,), p.dtype, "draft"))
+        i32 = lambda n: torch.empty(n, dtype=torch.int32, device=p.device)  # noqa: E731
+        self.accepted, self.out_tokens = i32(R), i32(T)
+        self.next_slots = prob.get("next_slots")
+        if self.next_slots is None and slots is not None:
+            self.next_slots = torch.full((R,), -1, dtype=torch.int32, device=p.device)
+        self.err = torch.zeros(4, dtype=torch.int32, device=p.device)
+        self.io = ssd_verify_io(_ptr(p), _ptr(q), _ptr(prob["tokens"]), _ptr(prob["accept_u"]),
+                                _ptr(prob["sample_u"]), _ptr(slots), _ptr(self.accepted), _ptr(self.out_tokens),
+                                _ptr(self.next_slots), _ptr(self.err))
+        self.stream = stream
+
+    def __call__(self):
+        ssd_varlen_verify(self.dims, self.prob["cu_seqlens"], self.io, self.stream)
+        return self
+
+    def status(self) -> int:
+        v = int(self.err[0].item())
+        self.err.zero_()
+        return v
+
+
+def run_verify(prob: dict, **kw) -> VerifyCall:
+    """One verification on the current stream; returns the VerifyCall (outputs on it)."""
+    return VerifyCall(prob, **kw)()

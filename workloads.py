@@ -611,3 +611,152 @@ def to_oracle_gdn(prob: dict, requests=None, heads=None) -> dict:
            "export_chunks": bool(prob.get("export_chunks")), "scale": prob.get("scale"),
            "l2norm": bool(prob.get("l2norm")), "requests": sel, "heads": hsel, "tokens": toks.numpy()}
     return out
+
+
+# ---- selective scan (S6), its windows, their convolution, draft verification --
+def _layout(t, how):
+    """t as it is ("dense"), or as a slice of a wider buffer: rows "wide" apart (16-byte aligned), or "odd"
+    elements apart and off any alignment but the element's."""
+    if how == "dense" or t is None:
+        return t
+    rows, n = t.shape[0], t[0].numel() if t.shape[0] else 0
+    pad, lead = (64, 16) if how == "wide" else (7, 3)
+    wide = torch.zeros((rows, (n + 63) // 64 * 64 + pad if how == "wide" else n + pad), dtype=t.dtype,
+                       device=t.device)
+    wide[:, lead:lead + n] = t.reshape(rows, n)
+    return wide[:, lead:lead + n].unflatten(1, t.shape[1:]) if t.dim() > 2 else wide[:, lead:lead + n]
+
+
+def _selective_layer(T, D, N, G, dtype, gen, dev, z, skip, bias, softplus, layout):
+    dt_ = torch.float32 if dtype == "fp32" else torch.bfloat16
+    step = torch.exp(torch.rand(D, generator=gen, device=dev) * float(np.log(100.0)) + float(np.log(1e-3)))
+    if softplus:
+        delta, b = _randn((T, D), gen, dev, dt_, 0.5), torch.log(torch.expm1(step))
+    else:
+        delta, b = (step * torch.exp(_randn((T, D), gen, dev, torch.float32, 0.5))).to(dt_), step * 0.1
+    A = -torch.arange(1, N + 1, device=dev, dtype=torch.float32) * torch.exp(_randn((D, N), gen, dev, torch.float32,
+                                                                                      0.1))
+    return {"u": _layout(_randn((T, D), gen, dev, dt_), layout), "delta": _layout(delta, layout),
+            "B": _layout(_randn((T, G, N), gen, dev, dt_), layout),
+            "C": _layout(_randn((T, G, N), gen, dev, dt_), layout),
+            "z": _layout(_randn((T, D), gen, dev, dt_), layout) if z else None, "A": A.contiguous(),
+            "D": _randn((D,), gen, dev, torch.float32) if skip else None, "delta_bias": b if bias else None,
+            "softplus": softplus, "dtype": dtype}
+
+
+def _cumulative(lens, dev):
+    cu = torch.zeros(len(lens) + 1, dtype=torch.int32)
+    cu[1:] = torch.cumsum(torch.tensor(lens, dtype=torch.int64), 0).to(torch.int32)
+    return cu.to(dev)
+
+
+def make_selective_problem(lengths, D, N=16, G=1, dtype="bf16", seed=0, device="cpu", z=True, skip=True, bias=True,
+                           softplus=True, layout="dense", init_every=2, final_slots=True, block_size=0,
+                           num_computed=None, canary=0.0) -> dict:
+    """A packed selective-scan prefill: every init_every-th request starts from a pool slot (0: none does), final
+    states go to slots of their own, and with block_size every block boundary has a slot; canary fills the slots
+    that the call may write."""
+    lens, dev = list(lengths), torch.device(device)
+    R, T = len(lens), int(sum(lens))
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(seed)
+    prob = _selective_layer(T, D, N, G, dtype, gen, dev, z, skip, bias, softplus, layout)
+    done = [0] * R if num_computed is None else list(num_computed)
+    init = [i for i in range(R) if init_every and i % init_every == 0]
+    bounds = [(i, kb) for i in range(R) for kb in range(1, (done[i] + lens[i]) // block_size + 1)
+              if kb * block_size > done[i]] if block_size else []
+    order = np.random.default_rng(seed).permutation(len(init) + (R if final_slots else 0) + len(bounds)).tolist()
+    pool = torch.full((max(len(order), 1), D, N), canary, dtype=torch.float32, device=dev)
+    prob.update(cu_seqlens=_cumulative(lens, dev), lengths=lens, T=T, R=R, state_pool=pool, block_size=block_size,
+                num_computed=None if num_computed is None else torch.tensor(done, dtype=torch.int32, device=dev),
+                init_slots=None, final_slots=None, block_table=None)
+    if init:
+        slots = [-1] * R
+        for i in init:
+            slots[i] = order.pop()
+            pool[slots[i]] = _randn((D, N), gen, dev, torch.float32, 0.5)
+        prob["init_slots"] = torch.tensor(slots, dtype=torch.int32, device=dev)
+    if final_slots:
+        prob["final_slots"] = torch.tensor([order.pop() for _ in range(R)], dtype=torch.int32, device=dev)
+    if block_size:
+        table = np.full((R, max([kb for _, kb in bounds], default=1)), -1, np.int32)
+        for i, kb in bounds:
+            table[i, kb - 1] = order.pop()
+        prob["block_table"] = torch.tensor(table, device=dev)
+    return prob
+
+
+def _anchors(R, T, seed, zero_every, skip_every, dev):
+    """Read slots for R requests (every zero_every-th -1), write slots for T tokens (every skip_every-th -1)."""
+    perm = np.random.default_rng(seed).permutation(R + T).astype(np.int32)
+    read, write = perm[:R].copy(), perm[R:].copy()
+    if zero_every:
+        read[zero_every - 1::zero_every] = -1
+    if skip_every:
+        write[skip_every - 1::skip_every] = -1
+    return torch.tensor(read, device=dev), torch.tensor(write, device=dev)
+
+
+def make_selective_step_problem(windows, D, N=16, G=1, dtype="bf16", seed=0, device="cpu", z=True, skip=True,
+                                bias=True, softplus=True, layout="dense", zero_every=3, skip_every=4) -> dict:
+    """A selective-scan step over windows of the given lengths, with read and write anchors."""
+    lens, dev = list(windows), torch.device(device)
+    R, T = len(lens), int(sum(lens))
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(seed)
+    prob = _selective_layer(T, D, N, G, dtype, gen, dev, z, skip, bias, softplus, layout)
+    read, write = _anchors(R, T, seed, zero_every, skip_every, dev)
+    prob.update(cu_seqlens=_cumulative(lens, dev), lengths=lens, T=T, R=R, read_slots=read, write_slots=write,
+                state_pool=_randn((R + T, D, N), gen, dev, torch.float32, 0.5))
+    return prob
+
+
+def make_conv_step_problem(windows, D, W=4, dtype="bf16", seed=0, device="cpu", silu=True, bias=True, zero_every=3,
+                           skip_every=4) -> dict:
+    """A causal conv1d step over windows of the given lengths: a write slot for every token."""
+    lens, dev = list(windows), torch.device(device)
+    R, T = len(lens), int(sum(lens))
+    dt_ = torch.float32 if dtype == "fp32" else torch.bfloat16
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(seed)
+    read, write = _anchors(R, T, seed, zero_every, skip_every, dev)
+    return {"x": _randn((T, D), gen, dev, dt_), "weight": _randn((D, W), gen, dev, torch.float32, 0.5),
+            "bias": _randn((D,), gen, dev, torch.float32, 0.5) if bias else None, "silu": silu, "dtype": dtype,
+            "cu_seqlens": _cumulative(lens, dev), "lengths": lens, "T": T, "R": R, "D": D, "W": W,
+            "conv_pool": _randn((R + T, D, W - 1), gen, dev, dt_), "read_slots": read, "write_slots": write}
+
+
+def make_verify_problem(windows, V, dtype="fp32", seed=0, device="cpu", draft=True, keep=0, near=0.5, scale=2.0,
+                        layout="dense") -> dict:
+    """Windows of drafted tokens with the target's and the draft's distributions (a draft model `near` the target's
+    logits; draft=False: drafts that have no distribution); keep > 0 leaves the target's `keep` likeliest tokens."""
+    lens, dev = list(windows), torch.device(device)
+    R, T = len(lens), int(sum(lens))
+    dt_ = torch.float32 if dtype == "fp32" else torch.bfloat16
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(seed)
+    x = _randn((T, V), gen, dev, torch.float32, scale)
+    p = torch.softmax(x, -1)
+    if keep and T:
+        p = torch.where(p >= p.topk(min(keep, V), -1).values[:, -1:], p, torch.zeros_like(p))
+        p = p / p.sum(-1, keepdim=True)
+    q = torch.softmax(x + _randn((T, V), gen, dev, torch.float32, near), -1)
+    drawn = torch.multinomial(q, 1, generator=gen).reshape(-1) if T else torch.zeros(0, device=dev)
+    return {"target": _layout(p.to(dt_), layout), "draft": _layout(q.to(dt_), layout) if draft else None,
+            "tokens": torch.roll(drawn, 1).to(torch.int32), "cu_seqlens": _cumulative(lens, dev), "lengths": lens,
+            "accept_u": torch.rand(T, generator=gen, device=dev), "sample_u": torch.rand(R, generator=gen, device=dev),
+            "write_slots": torch.randperm(T, generator=gen, device=dev).to(torch.int32)}
+
+
+def to_oracle_plain(prob: dict) -> dict:
+    """Host copies of one of these problems: fp64 for floating tensors (fp32 for probabilities and random numbers,
+    which the verification's definition takes as they are)."""
+    out = {}
+    for k, v in prob.items():
+        if torch.is_tensor(v):
+            v = v.detach().cpu()
+            if v.is_floating_point():
+                v = v.float() if "sample_u" in prob else v.double()
+            v = v.numpy().copy()
+        out[k] = v
+    return out
