@@ -20,7 +20,7 @@ __device__ __forceinline__ float sel_step(float v, bool softplus) { return softp
 // Validates the sizes; fills the shape with resolved strides.  Shared by both entry points.
 inline int sel_shape(const ssd_selective_dims *d, bool has_z, SelShape *s) {
     if (d->reserved != 0) return SSD_ERR_DIMS;
-    if (d->T < 0 || d->T > 0x7fffffffLL || d->R < 1 || d->R > 65535 || d->D < 1 || d->D > (1 << 24) || d->N < 1 ||
+    if (d->T < 0 || d->T > 0x7fffff00LL || d->R < 1 || d->D < 1 || d->D > (1 << 24) || d->N < 1 ||
         d->G < 1 || d->num_slots < 0 || d->block_size < 0 || d->block_table_width < 0)
         return SSD_ERR_DIMS;
     if (d->D % d->G != 0) return SSD_ERR_GROUPS;
