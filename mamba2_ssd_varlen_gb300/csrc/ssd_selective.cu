@@ -9,22 +9,29 @@
 // because the decay differs for every channel and state.  The kernel is bound by
 // instruction issue and those pipes, not by memory, so its shape is chosen to spend as
 // few other instructions as possible:
-//   - a CTA walks the tokens of one request for 32 channels of one group, L lanes a
-//     channel, each with NP / L states in registers as packed fp32 pairs (two
-//     multiply-adds an issue slot);
-//   - u, delta, z and the rows of B and C arrive by tiles of 16 tokens through
-//     asynchronous copies, a tile ahead; B and C are widened to fp32 once a tile;
-//   - softplus, u dt', the skip term and the gate are computed by the L lanes of a channel
-//     for different tokens, two at a time in packed pairs, and exchanged by shuffles.
-#include "f32x2.cuh"
+//   - a CTA walks the tokens of one request for 32 channels of one group; a lane holds
+//     two neighbouring channels as one packed fp32 pair (two multiply-adds an issue slot,
+//     and u, delta, z and y move as pairs) and NP / L of their states, L lanes a pair;
+//   - u, delta and z arrive by tiles of 16 tokens through asynchronous copies, two tiles
+//     ahead; B and C through registers, a tile ahead, laid out in shared memory as the
+//     (B, B, C, C) that a packed pair multiplies by: one 16-byte load a state;
+//   - softplus, u dt', the skip term and the gate are computed by the L lanes of a pair
+//     for different tokens, and exchanged through shared memory.  They, and the sums over
+//     the L lanes, belong to the blocks of TB tokens after and before the one whose
+//     recurrence runs beside them, so that their latency hides behind it.
 #include "pdl.cuh"
 #include "selective.cuh"
+#include "special.cuh"
 
 namespace ssd {
 namespace {
 
 constexpr int kTile = 16;  // tokens staged at a time
 constexpr int kCh = 32;    // channels of a CTA
+constexpr int kPairs = kCh / 2;
+#ifndef SEL_MIN
+#define SEL_MIN 1
+#endif
 
 struct SelParams {
     SelShape s;
@@ -32,7 +39,8 @@ struct SelParams {
     ssd_selective_io io;
     int32_t tiles;   // channel tiles of a request: G * ceil((D / G) / 32)
     int32_t vec;     // u, delta, z: every tile row of a CTA starts on a 16-byte boundary
-    int32_t bc_vec;  // B, C: every row does, and is whole 16-byte vectors
+    int32_t bc_vec;  // B, C: every four states of a row start on a boundary of four elements
+    int32_t y_pair;  // y: every pair of channels starts on a boundary of two elements
 };
 
 __device__ __forceinline__ void cp16(void *smem, const void *gmem) {
@@ -44,7 +52,8 @@ __device__ __forceinline__ void cp4(void *smem, const void *gmem) {
                  : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory"); }
 
 template <typename T>
 __device__ __forceinline__ void cp_elem(T *smem, const T *gmem) {
@@ -52,43 +61,92 @@ __device__ __forceinline__ void cp_elem(T *smem, const T *gmem) {
     else *smem = *gmem;  // two bytes: no asynchronous copy is that small
 }
 
-// Shared memory of a CTA.
-template <typename T, int NP>
-struct Smem {
-    T raw[2][3][kTile][kCh];             // u, delta, z of two tiles
-    T bc[2][2][kTile][NP];               // B and C as they come
-    float f[2][kTile][NP];               // B and C of the tile at hand, fp32, zeros past N and past the tile
+template <bool v>
+struct Flag {
+    static constexpr bool value = v;
 };
 
-template <int L>
+// Two neighbouring elements to and from fp32.
+__device__ __forceinline__ float2 load_pair(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+__device__ __forceinline__ float2 load_pair(const __nv_bfloat16 *p) {
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ void store_pair(float *p, float2 v) { *reinterpret_cast<float2 *>(p) = v; }
+__device__ __forceinline__ void store_pair(__nv_bfloat16 *p, float2 v) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
+}
+
+// Four neighbouring elements in registers.
+template <typename T>
+struct Four;
+template <>
+struct Four<float> {
+    float4 v;
+    __device__ __forceinline__ void load(const float *p) { v = *reinterpret_cast<const float4 *>(p); }
+    __device__ __forceinline__ void set(int j, float x) { (&v.x)[j] = x; }
+    __device__ __forceinline__ float4 get() const { return v; }
+};
+template <>
+struct Four<__nv_bfloat16> {
+    uint2 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void set(int j, __nv_bfloat16 x) {
+        const uint32_t b = *reinterpret_cast<const unsigned short *>(&x);
+        uint32_t &w = j < 2 ? v.x : v.y;
+        w = j & 1 ? (w & 0xFFFFu) | b << 16 : (w & 0xFFFF0000u) | b;
+    }
+    __device__ __forceinline__ float4 get() const {
+        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                           __uint_as_float(v.y & 0xFFFF0000u));
+    }
+};
+
+// L lanes a pair of channels (lane = l * PW + pair in a warp of PW pairs); blocks of TB
+// tokens, OWN of them each lane's own.
+template <typename T, int NP, int L>
+struct Cfg {
+    static constexpr int NS = NP / L;              // states of a lane
+    static constexpr int PW = 32 / L;              // pairs of a warp
+    static constexpr int OWN = L < 4 ? 4 / L : 1;
+    static constexpr int TB = OWN * L;
+    static constexpr int THREADS = kPairs * L;
+    static constexpr int WARPS = (THREADS + 31) / 32;
+    static constexpr int QUADS = kTile * NP / 4;   // (row, four states) of a tile of B or C
+    static constexpr int IT = (QUADS + THREADS - 1) / THREADS;
+    static_assert(NS >= 1 && kTile % TB == 0 && L <= 16, "whole blocks, a pair inside a warp");
+    struct Smem {
+        T raw[3][3][kTile][kCh];        // u, delta, z of the tile at hand, the next and the one in flight
+        float2 f[2][kTile][NP];         // (B, C) of the tile at hand and the next; zeros past N
+        float4 dd[2][WARPS][TB][PW];    // dt' and dt' u of each pair: the block at hand and the next
+        float2 yp[2][WARPS][TB][32];    // a block's partial sums, [token][lane]
+    };
+};
+
+template <int THREADS>
 __device__ __forceinline__ void cta_sync() {
-    if constexpr (L == 1) __syncwarp();
+    if constexpr (THREADS <= 32) __syncwarp();
     else __syncthreads();
 }
 
-// L lanes a channel; lane = l * CW + c in a warp of CW = 32 / L channels.
-template <typename T, int NP, int L>
-__global__ void __launch_bounds__(kCh * L) selective_kernel(const __grid_constant__ SelParams p) {
-    constexpr int NS = NP / L;               // states of a lane
-    constexpr int NK = NS / 2;               // as packed pairs
-    constexpr int CW = 32 / L;               // channels of a warp
-    constexpr int OWN = L == 1 ? 4 : 2;      // tokens of a block whose step and gate a lane computes
-    constexpr int TB = OWN * L;              // tokens of a block
-    constexpr int THREADS = kCh * L;
-    static_assert(NS >= 2 && kTile % TB == 0, "pairs of states, whole blocks");
+template <typename T, int NP, int L, bool kSoftplus, bool kGate>
+__global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __grid_constant__ SelParams p) {
+    using K = Cfg<T, NP, L>;
+    constexpr int NS = K::NS, PW = K::PW, OWN = K::OWN, TB = K::TB, THREADS = K::THREADS, IT = K::IT;
     extern __shared__ __align__(16) uint8_t sel_smem[];
-    Smem<T, NP> &sm = *reinterpret_cast<Smem<T, NP> *>(sel_smem);
+    typename K::Smem &sm = *reinterpret_cast<typename K::Smem *>(sel_smem);
     pdl_wait();
     const SelShape &s = p.s;
     const ssd_selective_io &io = p.io;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int l = lane / CW, c = warp * CW + lane % CW;  // this lane's share of the states, its channel in the tile
+    const int l = lane / PW, pr = lane % PW;       // this lane's share of the states, its pair in the warp
+    const int c = (warp * PW + pr) * 2;            // the pair's first channel in the tile
     const int i = (int)(blockIdx.x / p.tiles), tile = (int)(blockIdx.x % p.tiles);
     const int dg = s.D / s.G, per_group = p.tiles / s.G;
     const int g = tile / per_group, off = (tile % per_group) * kCh;
-    const int width = min(kCh, dg - off);    // channels of this CTA
+    const int width = min(kCh, dg - off);          // channels of this CTA
     const int d0 = g * dg + off, d = d0 + c;
-    const bool mine = c < width;
+    const bool mine[2] = {c < width, c + 1 < width};
     const bool first = tile == 0 && tid == 0;
 
     const int64_t a = p.cu[i], b = p.cu[i + 1];
@@ -109,26 +167,28 @@ __global__ void __launch_bounds__(kCh * L) selective_kernel(const __grid_constan
     }
 
     const T *gu = static_cast<const T *>(io.u) + a * s.us + d0, *gd = static_cast<const T *>(io.delta) + a * s.ds + d0;
-    const T *gz = io.z ? static_cast<const T *>(io.z) + a * s.zs + d0 : nullptr;
+    const T *gz = kGate ? static_cast<const T *>(io.z) + a * s.zs + d0 : nullptr;
     const T *gb = static_cast<const T *>(io.B) + a * s.bs + (size_t)g * s.N;
     const T *gc = static_cast<const T *>(io.C) + a * s.cs + (size_t)g * s.N;
     T *gy = static_cast<T *>(io.y) + a * s.ys + d;
 
     // Tiles end at absolute multiples of kTile where block states are kept, so that a boundary ends its tile.
     const int lead = table ? done % kTile : 0;
+    const int tiles = (lead + len + kTile - 1) / kTile;
     auto tile_begin = [&](int k) { return k == 0 ? 0 : k * kTile - lead; };
-    auto stage = [&](int k) {  // asynchronous copies of tile k
-        const int t0 = tile_begin(k), n = min(len, (k + 1) * kTile - lead) - t0, st = k & 1;
-        constexpr int E = 16 / sizeof(T);    // elements of a vector
+    auto rows_of = [&](int k) { return min(len, (k + 1) * kTile - lead) - tile_begin(k); };
+    auto stage = [&](int k) {  // asynchronous copies of u, delta and z of tile k
+        const int t0 = tile_begin(k), n = rows_of(k), st = k % 3;
+        constexpr int E = 16 / sizeof(T);  // elements of a vector
         if (p.vec) {
-            constexpr int V = kCh / E;       // vectors of a row
+            constexpr int V = kCh / E;     // vectors of a row
             for (int q = tid; q < n * V; q += THREADS) {
                 const int r = q / V, col = q % V * E;
                 if (col >= width) continue;
                 const size_t t = t0 + r;
                 cp16(&sm.raw[st][0][r][col], gu + t * s.us + col);
                 cp16(&sm.raw[st][1][r][col], gd + t * s.ds + col);
-                if (gz) cp16(&sm.raw[st][2][r][col], gz + t * s.zs + col);
+                if (kGate) cp16(&sm.raw[st][2][r][col], gz + t * s.zs + col);
             }
         } else {
             for (int q = tid; q < n * kCh; q += THREADS) {
@@ -137,30 +197,49 @@ __global__ void __launch_bounds__(kCh * L) selective_kernel(const __grid_constan
                 const size_t t = t0 + r;
                 cp_elem(&sm.raw[st][0][r][col], gu + t * s.us + col);
                 cp_elem(&sm.raw[st][1][r][col], gd + t * s.ds + col);
-                if (gz) cp_elem(&sm.raw[st][2][r][col], gz + t * s.zs + col);
-            }
-        }
-        if (p.bc_vec) {
-            const int V = s.N / E;
-            for (int q = tid; q < n * V; q += THREADS) {
-                const int r = q / V, col = q % V * E;
-                cp16(&sm.bc[st][0][r][col], gb + (size_t)(t0 + r) * s.bs + col);
-                cp16(&sm.bc[st][1][r][col], gc + (size_t)(t0 + r) * s.cs + col);
-            }
-        } else {
-            for (int q = tid; q < n * s.N; q += THREADS) {
-                const int r = q / s.N, col = q % s.N;
-                cp_elem(&sm.bc[st][0][r][col], gb + (size_t)(t0 + r) * s.bs + col);
-                cp_elem(&sm.bc[st][1][r][col], gc + (size_t)(t0 + r) * s.cs + col);
+                if (kGate) cp_elem(&sm.raw[st][2][r][col], gz + t * s.zs + col);
             }
         }
         cp_commit();
+    };
+    Four<T> bq[IT], cq[IT];            // B and C of the next tile on their way
+    auto fetch_bc = [&](int k) {
+        const int t0 = tile_begin(k), n = rows_of(k);
+#pragma unroll
+        for (int q = 0; q < IT; ++q) {
+            const int e = tid + q * THREADS, r = e / (NP / 4), n4 = e % (NP / 4) * 4;
+            bq[q] = {}, cq[q] = {};
+            if (e >= K::QUADS || r >= n || n4 >= s.N) continue;
+            const T *sb = gb + (size_t)(t0 + r) * s.bs + n4, *sc = gc + (size_t)(t0 + r) * s.cs + n4;
+            if (p.bc_vec) {
+                bq[q].load(sb);
+                cq[q].load(sc);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (n4 + j < s.N) {
+                        bq[q].set(j, sb[j]);
+                        cq[q].set(j, sc[j]);
+                    }
+            }
+        }
+    };
+    auto widen_bc = [&](int k) {
+#pragma unroll
+        for (int q = 0; q < IT; ++q) {
+            const int e = tid + q * THREADS, r = e / (NP / 4), n4 = e % (NP / 4) * 4;
+            if (e >= K::QUADS) continue;
+            const float4 bv = bq[q].get(), cv = cq[q].get();
+            float4 *dst = reinterpret_cast<float4 *>(&sm.f[k & 1][r][n4]);
+            dst[0] = make_float4(bv.x, cv.x, bv.y, cv.y);
+            dst[1] = make_float4(bv.z, cv.z, bv.w, cv.w);
+        }
     };
 
     // The lane's states and decay rates (zeros past N and past the width: they stay zero).
     const size_t dn = (size_t)s.D * s.N, row = (size_t)d * s.N;
     const int n0 = l * NS;
-    f2 h[NK], A[NK];
+    float2 h[NS], A[NS];
     {
         const float *src = nullptr;
         if (io.init_slots) {
@@ -172,127 +251,186 @@ __global__ void __launch_bounds__(kCh * L) selective_kernel(const __grid_constan
             }
         }
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
+        for (int k = 0; k < NS; ++k) {
             float hv[2], av[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int n = n0 + 2 * k + e;
-                const bool ok = mine && n < s.N;
-                hv[e] = ok && src ? src[n] : 0.f;
-                av[e] = ok ? io.A[row + n] * kLog2e : 0.f;
+                const bool ok = mine[e] && n0 + k < s.N;
+                const size_t at = (size_t)e * s.N + n0 + k;
+                hv[e] = ok && src ? src[at] : 0.f;
+                av[e] = ok ? io.A[row + at] * kLog2e : 0.f;
             }
-            h[k] = pk(hv[0], hv[1]);
-            A[k] = pk(av[0], av[1]);
+            h[k] = make_float2(hv[0], hv[1]);
+            A[k] = make_float2(av[0], av[1]);
         }
     }
-    const float bias = mine && io.delta_bias ? io.delta_bias[d] : 0.f, skip = mine && io.D ? io.D[d] : 0.f;
+    auto two = [&](const float *v) { return make_float2(v && mine[0] ? v[d] : 0.f, v && mine[1] ? v[d + 1] : 0.f); };
+    const float2 bias = two(io.delta_bias), skip = two(io.D);
     auto put = [&](float *base) {
-        if (!mine) return;
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
-            const float2 v = upk(h[k]);
-            const int n = n0 + 2 * k;
-            if (n < s.N) base[row + n] = v.x;
-            if (n + 1 < s.N) base[row + n + 1] = v.y;
+        for (int k = 0; k < NS; ++k) {
+            if (n0 + k < s.N) {
+                if (mine[0]) base[row + n0 + k] = h[k].x;
+                if (mine[1]) base[row + s.N + n0 + k] = h[k].y;
+            }
         }
     };
 
-    const int tiles = (lead + len + kTile - 1) / kTile;
-    if (len > 0) stage(0);
-    for (int k = 0; k < tiles && len > 0; ++k) {
-        const int t0 = tile_begin(k), n = min(len, (k + 1) * kTile - lead) - t0, st = k & 1;
-        cp_wait_all();
-        cta_sync<L>();  // tile k has landed; everybody is done with the buffers of tile k - 1
-        if (k + 1 < tiles) stage(k + 1);
-        for (int q = tid; q < 2 * kTile * NP; q += THREADS) {
-            const int r = q / NP % kTile, col = q % NP;
-            sm.f[q / (NP * kTile)][r][col] = r < n && col < s.N ? to_f32(sm.bc[st][q / (NP * kTile)][r][col]) : 0.f;
+    // What a lane keeps for its own tokens of a block until their sums are there.
+    struct Kept {
+        float2 uv[OWN], gate[OWN];
+    };
+    // Steps of the block whose rows start at r (the lane's own first row and pair of u), for exchange buffer x.
+    auto prepare = [&](const T *r, int x) {
+        Kept o;
+#pragma unroll
+        for (int q = 0; q < OWN; ++q) {
+            o.uv[q] = load_pair(r + q * kCh);
+            float2 v = load_pair(r + (kTile + q) * kCh);
+            v.x += bias.x;
+            v.y += bias.y;
+            if (kSoftplus) v = make_float2(softplus_sfu(v.x), softplus_sfu(v.y));
+            o.gate[q] = make_float2(0.f, 0.f);
+            if (kGate) {
+                const float2 z = load_pair(r + (2 * kTile + q) * kCh);
+                o.gate[q] = make_float2(silu_sfu(z.x), silu_sfu(z.y));
+            }
+            sm.dd[x][warp][l * OWN + q][pr] = make_float4(v.x, v.y, v.x * o.uv[q].x, v.y * o.uv[q].y);
         }
-        cta_sync<L>();
+        return o;
+    };
+    // The recurrence over a block, (B, C) from f on (its first `valid` tokens); partial sums to exchange buffer x.
+    auto advance = [&](const float2 *f, int x, int valid, auto full) {
+        float2 acc[TB];
+#pragma unroll
+        for (int j = 0; j < TB; ++j) {
+            acc[j] = make_float2(0.f, 0.f);
+            if (!full.value && j >= valid) continue;
+            const float4 dd = sm.dd[x][warp][j][pr];
+            float2 bc[NS];
+            if constexpr (NS == 1) {
+                bc[0] = f[j * NP];
+            } else {
+#pragma unroll
+                for (int q = 0; q < NS; q += 2) {
+                    const float4 v = *reinterpret_cast<const float4 *>(f + j * NP + q);
+                    bc[q] = make_float2(v.x, v.y);
+                    bc[q + 1] = make_float2(v.z, v.w);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < NS; ++q) {
+                h[q].x = fmaf(ex2f(dd.x * A[q].x), h[q].x, dd.z * bc[q].x);
+                h[q].y = fmaf(ex2f(dd.y * A[q].y), h[q].y, dd.w * bc[q].x);
+                acc[j].x = q == 0 ? h[q].x * bc[q].y : fmaf(h[q].x, bc[q].y, acc[j].x);
+                acc[j].y = q == 0 ? h[q].y * bc[q].y : fmaf(h[q].y, bc[q].y, acc[j].y);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < TB; ++j) sm.yp[x][warp][j][lane] = acc[j];
+    };
+    // Outputs of the block computed before, from exchange buffer x: the lane's own tokens among the `valid` first, y
+    // of the block's first token at dst.
+    auto finish = [&](const Kept &o, int x, T *dst, int valid, auto full) {
+#pragma unroll
+        for (int q = 0; q < OWN; ++q) {
+            const int j = l * OWN + q;
+            float2 out = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < L; ++e) {  // lane l starts with its own column: no two lanes in one bank
+                const float2 w = sm.yp[x][warp][j][lane ^ e * PW];
+                out.x += w.x;
+                out.y += w.y;
+            }
+            out.x = fmaf(skip.x, o.uv[q].x, out.x);
+            out.y = fmaf(skip.y, o.uv[q].y, out.y);
+            if (kGate) {
+                out.x *= o.gate[q].x;
+                out.y *= o.gate[q].y;
+            }
+            T *at = dst + (size_t)j * s.ys;
+            const bool there = full.value || j < valid;
+            if (p.y_pair) {
+                if (there && mine[1]) store_pair(at, out);
+            } else {
+                if (there && mine[0]) at[0] = from_f32<T>(out.x);
+                if (there && mine[1]) at[1] = from_f32<T>(out.y);
+            }
+        }
+    };
+
+    // Tile k is computed while tile k + 1 (landed) is prepared for and tile k + 2 is in flight.
+    if (tiles > 0 && len > 0) {
+        stage(0);
+        if (tiles > 1) stage(1);
+        fetch_bc(0);
+        widen_bc(0);
+        if (tiles > 1) cp_wait<1>();
+        else cp_wait<0>();
+        cta_sync<THREADS>();
+        int buf = 0;                                   // raw buffer of the tile at hand
+        auto raw_row = [&](int which, int j0) { return &sm.raw[which][0][j0 + l * OWN][c]; };
+        Kept now = prepare(raw_row(0, 0), 0), before = now;
+        T *before_y = gy;                              // y of the block computed last, and how many of its tokens
+        int before_valid = 0, x = 0;                   // are there; x: the exchange buffer of the block at hand
+        for (int k = 0; k < tiles; ++k) {
+            const int t0 = tile_begin(k), n = rows_of(k), buf1 = buf == 2 ? 0 : buf + 1;
+            cp_wait<0>();
+            cta_sync<THREADS>();  // tile k + 1 has landed, B and C of tile k are laid out, tile k - 1 is computed
+            if (k + 2 < tiles) stage(k + 2);
+            if (k + 1 < tiles) fetch_bc(k + 1);
+            T *ty = gy + (size_t)t0 * s.ys;
+            const float2 *f = &sm.f[k & 1][0][n0];
+            if (n == kTile) {     // whole tiles, unrolled: the exchange buffers alternate an even number of times
+                const T *r0 = raw_row(buf, 0), *r1 = raw_row(buf1, 0);
+                constexpr int NB = kTile / TB;
+                static_assert(NB % 2 == 0, "parity");
+#pragma unroll
+                for (int q = 0; q < NB; ++q) {
+                    const Kept next = prepare(q + 1 < NB ? r0 + (q + 1) * TB * kCh : r1, x ^ (q & 1) ^ 1);
+                    advance(f + q * TB * NP, x ^ (q & 1), TB, Flag<true>{});
+                    if (q == 0) finish(before, x ^ 1, before_y, before_valid, Flag<false>{});
+                    else finish(before, x ^ (q & 1) ^ 1, ty + (size_t)((q - 1) * TB) * s.ys, TB, Flag<true>{});
+                    before = now;
+                    now = next;
+                    __syncwarp();
+                }
+                before_y = ty + (size_t)(kTile - TB) * s.ys;
+                before_valid = TB;
+            } else {
 #pragma unroll 1
-        for (int j0 = 0; j0 < n; j0 += TB) {
-            // the steps of the lane's own tokens; zero past the tile, where they change nothing
-            f2 dt[OWN / 2], du[OWN / 2], uv[OWN / 2];
-#pragma unroll
-            for (int q = 0; q < OWN / 2; ++q) {
-                const int r = j0 + l * OWN + 2 * q;
-                const bool v0 = r < n, v1 = r + 1 < n;
-                uv[q] = pk(to_f32(sm.raw[st][0][r][c]), to_f32(sm.raw[st][0][r + 1][c]));
-                f2 v = add2(pk(to_f32(sm.raw[st][1][r][c]), to_f32(sm.raw[st][1][r + 1][c])), dup2(bias));
-                if (s.softplus) v = softplus2(v);
-                const float2 x = upk(v), m = upk(mul2(v, uv[q]));
-                dt[q] = pk(v0 ? x.x : 0.f, v1 ? x.y : 0.f);
-                du[q] = pk(v0 ? m.x : 0.f, v1 ? m.y : 0.f);
-            }
-            float y[TB];
-#pragma unroll
-            for (int j = 0; j < TB; ++j) {
-                const float2 dp = upk(dt[j % OWN / 2]), up = upk(du[j % OWN / 2]);
-                float dv = j % 2 ? dp.y : dp.x, uu = j % 2 ? up.y : up.x;
-                if constexpr (L > 1) {
-                    dv = __shfl_sync(0xffffffffu, dv, j / OWN * CW + lane % CW);
-                    uu = __shfl_sync(0xffffffffu, uu, j / OWN * CW + lane % CW);
+                for (int j0 = 0; j0 < n; j0 += TB) {
+                    const Kept next = prepare(j0 + TB < n ? raw_row(buf, j0 + TB) : raw_row(buf1, 0), x ^ 1);
+                    advance(f + j0 * NP, x, n - j0, Flag<false>{});
+                    finish(before, x ^ 1, before_y, before_valid, Flag<false>{});
+                    before = now;
+                    now = next;
+                    before_y = ty + (size_t)j0 * s.ys;
+                    before_valid = min(TB, n - j0);
+                    x ^= 1;
+                    __syncwarp();
                 }
-                const f2 dd = dup2(dv), ud = dup2(uu);
-                const f2 *B = reinterpret_cast<const f2 *>(&sm.f[0][j0 + j][n0]);
-                const f2 *C = reinterpret_cast<const f2 *>(&sm.f[1][j0 + j][n0]);
-                f2 acc = 0;
-#pragma unroll
-                for (int q = 0; q < NK; q += 2) {
-                    f2 b2[2], c2[2];
-                    if constexpr (NK >= 2) {
-                        const ulonglong2 bv = *reinterpret_cast<const ulonglong2 *>(B + q);
-                        const ulonglong2 cv = *reinterpret_cast<const ulonglong2 *>(C + q);
-                        b2[0] = bv.x, b2[1] = bv.y, c2[0] = cv.x, c2[1] = cv.y;
+            }
+            buf = buf1;
+            if (k + 1 < tiles) widen_bc(k + 1);
+            if (table) {
+                const int pos = done + t0 + n;
+                if (pos % s.block_size == 0) {
+                    const int col = pos / s.block_size - 1;
+                    if (col >= s.bt_width) {
+                        if (first) atomicOr(io.device_err, SSD_DEVERR_BLOCK_TABLE);
                     } else {
-                        b2[0] = B[0], c2[0] = C[0];
-                    }
-#pragma unroll
-                    for (int e = 0; e < (NK >= 2 ? 2 : 1); ++e) {
-                        h[q + e] = fma2(ex2_2(mul2(dd, A[q + e])), h[q + e], mul2(ud, b2[e]));
-                        acc = fma2(h[q + e], c2[e], acc);
-                    }
-                }
-                const float2 r = upk(acc);
-                y[j] = r.x + r.y;
-            }
-            // sums over the L lanes, each lane left with its own tokens'
-#pragma unroll
-            for (int w = L / 2; w >= 1; w /= 2) {
-                const bool up = (l & w) != 0;
-#pragma unroll
-                for (int j = 0; j < OWN * w; ++j) {
-                    const float lo = y[j], hi = y[j + OWN * w];
-                    y[j] = (up ? hi : lo) + __shfl_xor_sync(0xffffffffu, up ? lo : hi, w * CW);
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < OWN / 2; ++q) {
-                const int r = j0 + l * OWN + 2 * q;
-                f2 v = fma2(dup2(skip), uv[q], pk(y[2 * q], y[2 * q + 1]));
-                if (!io.D) v = pk(y[2 * q], y[2 * q + 1]);
-                if (gz) v = mul2(v, silu2(pk(to_f32(sm.raw[st][2][r][c]), to_f32(sm.raw[st][2][r + 1][c]))));
-                const float2 o = upk(v);
-                if (mine && r < n) gy[(size_t)(t0 + r) * s.ys] = from_f32<T>(o.x);
-                if (mine && r + 1 < n) gy[(size_t)(t0 + r + 1) * s.ys] = from_f32<T>(o.y);
-            }
-        }
-        if (table) {
-            const int pos = done + t0 + n;
-            if (pos % s.block_size == 0) {
-                const int col = pos / s.block_size - 1;
-                if (col >= s.bt_width) {
-                    if (first) atomicOr(io.device_err, SSD_DEVERR_BLOCK_TABLE);
-                } else {
-                    const int slot = io.block_table[(size_t)i * s.bt_width + col];
-                    if (slot >= s.num_slots) {
-                        if (first) atomicOr(io.device_err, SSD_DEVERR_BLOCK_SLOT);
-                    } else if (slot >= 0) {
-                        put(io.state_pool + (size_t)slot * dn);
+                        const int slot = io.block_table[(size_t)i * s.bt_width + col];
+                        if (slot >= s.num_slots) {
+                            if (first) atomicOr(io.device_err, SSD_DEVERR_BLOCK_SLOT);
+                        } else if (slot >= 0) {
+                            put(io.state_pool + (size_t)slot * dn);
+                        }
                     }
                 }
             }
         }
+        finish(before, x ^ 1, before_y, before_valid, Flag<false>{});
     }
     if (io.final_states) put(io.final_states + (size_t)i * dn);
     if (io.final_slots) {
@@ -305,26 +443,30 @@ __global__ void __launch_bounds__(kCh * L) selective_kernel(const __grid_constan
     }
 }
 
-template <typename T, int NP, int L>
-cudaError_t launch_k(const SelParams &p, cudaStream_t stream) {
-    constexpr size_t smem = sizeof(Smem<T, NP>);
+template <typename T, int NP, int L, bool kSoftplus, bool kGate>
+cudaError_t launch_g(const SelParams &p, cudaStream_t stream) {
+    constexpr auto kernel = selective_kernel<T, NP, L, kSoftplus, kGate>;
+    constexpr size_t smem = sizeof(typename Cfg<T, NP, L>::Smem);
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(selective_kernel<T, NP, L>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    return launch_after_prev(selective_kernel<T, NP, L>, dim3((unsigned)((int64_t)p.tiles * p.s.R)), dim3(kCh * L), smem,
-                             stream, p);
+    return launch_after_prev(kernel, dim3((unsigned)((int64_t)p.tiles * p.s.R)), dim3(kPairs * L), smem, stream, p);
+}
+
+template <typename T, int NP, int L>
+cudaError_t launch_k(const SelParams &p, cudaStream_t stream) {
+    if (p.s.softplus) return p.io.z ? launch_g<T, NP, L, true, true>(p, stream) : launch_g<T, NP, L, true, false>(p, stream);
+    return p.io.z ? launch_g<T, NP, L, false, true>(p, stream) : launch_g<T, NP, L, false, false>(p, stream);
 }
 
 #ifndef SEL_L16
-#define SEL_L16 2
+#define SEL_L16 4
 #endif
 
 template <typename T>
 cudaError_t launch(const SelParams &p, cudaStream_t stream) {
-    const int64_t ctas = (int64_t)p.tiles * p.s.R;
-    (void)ctas;
+    if (p.s.N <= 4) return launch_k<T, 4, 2>(p, stream);
     if (p.s.N <= 8) return launch_k<T, 8, 2>(p, stream);
     if (p.s.N <= 16) return launch_k<T, 16, SEL_L16>(p, stream);
     if (p.s.N <= 32) return launch_k<T, 32, 4>(p, stream);
@@ -375,7 +517,11 @@ extern "C" int ssd_varlen_selective_scan(const ssd_selective_dims *d, const int3
         return sel_aligned(ptr, 16) && stride * e % 16 == 0 && step * e % 16 == 0;
     };
     p.vec = rows16(io->u, p.s.us, dg) && rows16(io->delta, p.s.ds, dg) && (!io->z || rows16(io->z, p.s.zs, dg));
-    p.bc_vec = rows16(io->B, p.s.bs, d->N) && rows16(io->C, p.s.cs, d->N);
+    auto rows = [&](const void *ptr, int64_t stride, int64_t step, int64_t n) {  // on boundaries of n elements
+        return sel_aligned(ptr, n * e) && stride % n == 0 && step % n == 0;
+    };
+    p.bc_vec = rows(io->B, p.s.bs, d->N, 4) && rows(io->C, p.s.cs, d->N, 4);
+    p.y_pair = rows(io->y, p.s.ys, dg, 2);
     const cudaError_t err = d->dtype == SSD_DTYPE_BF16 ? launch<__nv_bfloat16>(p, stream) : launch<float>(p, stream);
     return err == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
