@@ -30,13 +30,15 @@ constexpr float kLn2 = 0.6931471805599453f;
 // s^2 <= 1/9 is cut after s^12 / 13 (the rest is below 2e-8), and which keeps its relative
 // accuracy for small e; exp(t) = 2^x (1 + t - x ln 2) with x = fl(t log2 e), so that the
 // rounding of x does not count.
-__device__ __forceinline__ float softplus_sfu(float v) {
+// In two halves, so that a caller can put other work behind 1 / (2 + e): e, then the rest from v, e and r = 1 / (2 + e).
+__device__ __forceinline__ float softplus_exp(float v) {
     const float t = max_nan(-fabsf(v), -200.f);  // e is 0 there
     const float x = t * kLog2e;
-    float e = ex2f(x);
-    e = fmaf(e, fmaf(x, -kLn2, t), e);
-    const float s = e * rcpf(e + 2.f);
-    const float q = s * s;
+    const float e = ex2f(x);
+    return fmaf(e, fmaf(x, -kLn2, t), e);
+}
+__device__ __forceinline__ float softplus_end(float v, float e, float r) {
+    const float s = e * r, q = s * s;
     float p = fmaf(q, 2.f / 13.f, 2.f / 11.f);
     p = fmaf(p, q, 2.f / 9.f);
     p = fmaf(p, q, 2.f / 7.f);

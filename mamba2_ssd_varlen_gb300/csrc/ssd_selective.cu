@@ -129,7 +129,8 @@ __device__ __forceinline__ void cta_sync() {
     else __syncthreads();
 }
 
-template <typename T, int NP, int L, bool kSoftplus, bool kGate>
+// kCommon: softplus, a gate, and pairs of y on their boundaries (what a layer has); else these are looked up.
+template <typename T, int NP, int L, bool kCommon>
 __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __grid_constant__ SelParams p) {
     using K = Cfg<T, NP, L>;
     constexpr int NS = K::NS, PW = K::PW, OWN = K::OWN, TB = K::TB, THREADS = K::THREADS, IT = K::IT;
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
     }
 
     const T *gu = static_cast<const T *>(io.u) + a * s.us + d0, *gd = static_cast<const T *>(io.delta) + a * s.ds + d0;
-    const T *gz = kGate ? static_cast<const T *>(io.z) + a * s.zs + d0 : nullptr;
+    const T *gz = kCommon || io.z ? static_cast<const T *>(io.z) + a * s.zs + d0 : nullptr;
     const T *gb = static_cast<const T *>(io.B) + a * s.bs + (size_t)g * s.N;
     const T *gc = static_cast<const T *>(io.C) + a * s.cs + (size_t)g * s.N;
     T *gy = static_cast<T *>(io.y) + a * s.ys + d;
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
                 const size_t t = t0 + r;
                 cp16(&sm.raw[st][0][r][col], gu + t * s.us + col);
                 cp16(&sm.raw[st][1][r][col], gd + t * s.ds + col);
-                if (kGate) cp16(&sm.raw[st][2][r][col], gz + t * s.zs + col);
+                if (kCommon || gz) cp16(&sm.raw[st][2][r][col], gz + t * s.zs + col);
             }
         } else {
             for (int q = tid; q < n * kCh; q += THREADS) {
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
                 const size_t t = t0 + r;
                 cp_elem(&sm.raw[st][0][r][col], gu + t * s.us + col);
                 cp_elem(&sm.raw[st][1][r][col], gd + t * s.ds + col);
-                if (kGate) cp_elem(&sm.raw[st][2][r][col], gz + t * s.zs + col);
+                if (kCommon || gz) cp_elem(&sm.raw[st][2][r][col], gz + t * s.zs + col);
             }
         }
         cp_commit();
@@ -276,85 +277,71 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
         }
     };
 
-    // What a lane keeps for its own tokens of a block until their sums are there.
-    struct Kept {
+    // A lane's own tokens of a block on their way from the staged rows to the exchange buffer (`steps`), and what it
+    // keeps of them until their sums are there.
+    struct Own {
         float2 uv[OWN], gate[OWN];
     };
-    // Steps of the block whose rows start at r (the lane's own first row and pair of u), for exchange buffer x.
-    auto prepare = [&](const T *r, int x) {
-        Kept o;
+    struct Steps {
+        float2 v[OWN], e[OWN], r[OWN], z[OWN], ze[OWN];
+    };
+    const bool softplus = kCommon || s.softplus, gated = kCommon || gz != nullptr;
+    // Four stages, each taking up what the special-function unit gave the one before it.
+    auto prepare = [&](int stage, Own &o, Steps &w, const T *r, int x) {
 #pragma unroll
         for (int q = 0; q < OWN; ++q) {
-            o.uv[q] = load_pair(r + q * kCh);
-            float2 v = load_pair(r + (kTile + q) * kCh);
-            v.x += bias.x;
-            v.y += bias.y;
-            if (kSoftplus) v = make_float2(softplus_sfu(v.x), softplus_sfu(v.y));
-            o.gate[q] = make_float2(0.f, 0.f);
-            if (kGate) {
-                const float2 z = load_pair(r + (2 * kTile + q) * kCh);
-                o.gate[q] = make_float2(silu_sfu(z.x), silu_sfu(z.y));
-            }
-            sm.dd[x][warp][l * OWN + q][pr] = make_float4(v.x, v.y, v.x * o.uv[q].x, v.y * o.uv[q].y);
-        }
-        return o;
-    };
-    // The recurrence over a block, (B, C) from f on (its first `valid` tokens); partial sums to exchange buffer x.
-    auto advance = [&](const float2 *f, int x, int valid, auto full) {
-        float2 acc[TB];
-#pragma unroll
-        for (int j = 0; j < TB; ++j) {
-            acc[j] = make_float2(0.f, 0.f);
-            if (!full.value && j >= valid) continue;
-            const float4 dd = sm.dd[x][warp][j][pr];
-            float2 bc[NS];
-            if constexpr (NS == 1) {
-                bc[0] = f[j * NP];
+            if (stage == 0) {
+                o.uv[q] = load_pair(r + q * kCh);
+                w.v[q] = load_pair(r + (kTile + q) * kCh);
+                w.v[q].x += bias.x;
+                w.v[q].y += bias.y;
+                if (gated) w.z[q] = load_pair(r + (2 * kTile + q) * kCh);
+            } else if (stage == 1) {
+                if (softplus) w.e[q] = make_float2(softplus_exp(w.v[q].x), softplus_exp(w.v[q].y));
+                if (gated) w.ze[q] = make_float2(ex2f(-kLog2e * w.z[q].x), ex2f(-kLog2e * w.z[q].y));
+            } else if (stage == 2) {
+                if (softplus) w.r[q] = make_float2(rcpf(w.e[q].x + 2.f), rcpf(w.e[q].y + 2.f));
+                if (gated) o.gate[q] = make_float2(rcpf(1.f + w.ze[q].x), rcpf(1.f + w.ze[q].y));
             } else {
-#pragma unroll
-                for (int q = 0; q < NS; q += 2) {
-                    const float4 v = *reinterpret_cast<const float4 *>(f + j * NP + q);
-                    bc[q] = make_float2(v.x, v.y);
-                    bc[q + 1] = make_float2(v.z, v.w);
+                if (softplus)
+                    w.v[q] = make_float2(softplus_end(w.v[q].x, w.e[q].x, w.r[q].x),
+                                         softplus_end(w.v[q].y, w.e[q].y, w.r[q].y));
+                if (gated) {
+                    o.gate[q].x *= w.z[q].x;
+                    o.gate[q].y *= w.z[q].y;
                 }
-            }
-#pragma unroll
-            for (int q = 0; q < NS; ++q) {
-                h[q].x = fmaf(ex2f(dd.x * A[q].x), h[q].x, dd.z * bc[q].x);
-                h[q].y = fmaf(ex2f(dd.y * A[q].y), h[q].y, dd.w * bc[q].x);
-                acc[j].x = q == 0 ? h[q].x * bc[q].y : fmaf(h[q].x, bc[q].y, acc[j].x);
-                acc[j].y = q == 0 ? h[q].y * bc[q].y : fmaf(h[q].y, bc[q].y, acc[j].y);
+                sm.dd[x][warp][l * OWN + q][pr] =
+                    make_float4(w.v[q].x, w.v[q].y, w.v[q].x * o.uv[q].x, w.v[q].y * o.uv[q].y);
             }
         }
-#pragma unroll
-        for (int j = 0; j < TB; ++j) sm.yp[x][warp][j][lane] = acc[j];
     };
-    // Outputs of the block computed before, from exchange buffer x: the lane's own tokens among the `valid` first, y
-    // of the block's first token at dst.
-    auto finish = [&](const Kept &o, int x, T *dst, int valid, auto full) {
+    // Outputs of the block computed before, from exchange buffer x, in two stages: the sums of the lane's own tokens,
+    // then those of the `valid` first tokens to memory (the lane's first at dst).
+    auto finish = [&](int stage, float2 (&out)[OWN], const Own &o, int x, T *dst, int valid) {
 #pragma unroll
         for (int q = 0; q < OWN; ++q) {
             const int j = l * OWN + q;
-            float2 out = make_float2(0.f, 0.f);
+            if (stage == 0) {
+                out[q] = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < L; ++e) {  // lane l starts with its own column: no two lanes in one bank
-                const float2 w = sm.yp[x][warp][j][lane ^ e * PW];
-                out.x += w.x;
-                out.y += w.y;
-            }
-            out.x = fmaf(skip.x, o.uv[q].x, out.x);
-            out.y = fmaf(skip.y, o.uv[q].y, out.y);
-            if (kGate) {
-                out.x *= o.gate[q].x;
-                out.y *= o.gate[q].y;
-            }
-            T *at = dst + (size_t)j * s.ys;
-            const bool there = full.value || j < valid;
-            if (p.y_pair) {
-                if (there && mine[1]) store_pair(at, out);
+                for (int e = 0; e < L; ++e) {  // lane l starts with its own column: no two lanes in one bank
+                    const float2 w = sm.yp[x][warp][j][lane ^ e * PW];
+                    out[q].x += w.x;
+                    out[q].y += w.y;
+                }
             } else {
-                if (there && mine[0]) at[0] = from_f32<T>(out.x);
-                if (there && mine[1]) at[1] = from_f32<T>(out.y);
+                float2 v = make_float2(fmaf(skip.x, o.uv[q].x, out[q].x), fmaf(skip.y, o.uv[q].y, out[q].y));
+                if (gated) {
+                    v.x *= o.gate[q].x;
+                    v.y *= o.gate[q].y;
+                }
+                T *at = dst + (size_t)q * s.ys;
+                if (kCommon || p.y_pair) {
+                    if (j < valid && mine[1]) store_pair(at, v);
+                } else {
+                    if (j < valid && mine[0]) at[0] = from_f32<T>(v.x);
+                    if (j < valid && mine[1]) at[1] = from_f32<T>(v.y);
+                }
             }
         }
     };
@@ -368,48 +355,90 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
         if (tiles > 1) cp_wait<1>();
         else cp_wait<0>();
         cta_sync<THREADS>();
-        int buf = 0;                                   // raw buffer of the tile at hand
-        auto raw_row = [&](int which, int j0) { return &sm.raw[which][0][j0 + l * OWN][c]; };
-        Kept now = prepare(raw_row(0, 0), 0), before = now;
-        T *before_y = gy;                              // y of the block computed last, and how many of its tokens
-        int before_valid = 0, x = 0;                   // are there; x: the exchange buffer of the block at hand
+        int buf = 0;                       // raw buffer of the tile at hand
+        auto raw_row = [&](int which) { return &sm.raw[which][0][l * OWN][c]; };
+        Own before = {}, now, next;        // the block computed last, the one at hand, the one prepared beside it
+        {
+            Steps w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) prepare(e, now, w, raw_row(0), 0);
+        }
+        T *yp = gy + (int64_t)(l * OWN - TB) * s.ys;  // y of the lane's first token in the block before
+        int before_valid = 0;                         // and how many of that block's tokens there are
+        const int64_t y_step = (int64_t)TB * s.ys;
+        // One block of tile k: the recurrence of its tokens, and between them, a stage at a time, the steps of the next
+        // block (rows from r on) and the outputs of the one before.  x: the exchange buffer of this block.
+        auto block = [&](const float2 *f, const T *r, int x, int valid, auto full) {
+            Steps w;
+            float2 acc[TB], out[OWN];
+            finish(0, out, before, x ^ 1, yp, before_valid);
+            prepare(0, next, w, r, x ^ 1);
+#pragma unroll
+            for (int j = 0; j < TB; ++j) {
+                acc[j] = make_float2(0.f, 0.f);
+                if (full.value || j < valid) {
+                    const float4 dd = sm.dd[x][warp][j][pr];
+                    float2 bc[NS];
+                    if constexpr (NS == 1) {
+                        bc[0] = f[j * NP];
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < NS; q += 2) {
+                            const float4 v = *reinterpret_cast<const float4 *>(f + j * NP + q);
+                            bc[q] = make_float2(v.x, v.y);
+                            bc[q + 1] = make_float2(v.z, v.w);
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < NS; ++q) {
+                        h[q].x = fmaf(ex2f(dd.x * A[q].x), h[q].x, dd.z * bc[q].x);
+                        h[q].y = fmaf(ex2f(dd.y * A[q].y), h[q].y, dd.w * bc[q].x);
+                        acc[j].x = q == 0 ? h[q].x * bc[q].y : fmaf(h[q].x, bc[q].y, acc[j].x);
+                        acc[j].y = q == 0 ? h[q].y * bc[q].y : fmaf(h[q].y, bc[q].y, acc[j].y);
+                    }
+                }
+                if (j == 0) finish(1, out, before, x ^ 1, yp, before_valid);
+                if (TB <= 4) {
+                    if (j < 3) prepare(j + 1, next, w, r, x ^ 1);
+                } else if (j % (TB / 4) == 0 && j / (TB / 4) < 3) {
+                    prepare(j / (TB / 4) + 1, next, w, r, x ^ 1);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < TB; ++j) sm.yp[x][warp][j][lane] = acc[j];
+            before = now;
+            now = next;
+            before_valid = valid;
+            __syncwarp();
+        };
+        constexpr int NB = kTile / TB;     // blocks of a tile: an even number, so the exchange buffers alternate in step
+        static_assert(NB % 2 == 0, "parity");
         for (int k = 0; k < tiles; ++k) {
             const int t0 = tile_begin(k), n = rows_of(k), buf1 = buf == 2 ? 0 : buf + 1;
             cp_wait<0>();
             cta_sync<THREADS>();  // tile k + 1 has landed, B and C of tile k are laid out, tile k - 1 is computed
             if (k + 2 < tiles) stage(k + 2);
             if (k + 1 < tiles) fetch_bc(k + 1);
-            T *ty = gy + (size_t)t0 * s.ys;
             const float2 *f = &sm.f[k & 1][0][n0];
-            if (n == kTile) {     // whole tiles, unrolled: the exchange buffers alternate an even number of times
-                const T *r0 = raw_row(buf, 0), *r1 = raw_row(buf1, 0);
-                constexpr int NB = kTile / TB;
-                static_assert(NB % 2 == 0, "parity");
+            const T *r0 = raw_row(buf), *r1 = raw_row(buf1);
+            if (n == kTile) {
 #pragma unroll
                 for (int q = 0; q < NB; ++q) {
-                    const Kept next = prepare(q + 1 < NB ? r0 + (q + 1) * TB * kCh : r1, x ^ (q & 1) ^ 1);
-                    advance(f + q * TB * NP, x ^ (q & 1), TB, Flag<true>{});
-                    if (q == 0) finish(before, x ^ 1, before_y, before_valid, Flag<false>{});
-                    else finish(before, x ^ (q & 1) ^ 1, ty + (size_t)((q - 1) * TB) * s.ys, TB, Flag<true>{});
-                    before = now;
-                    now = next;
-                    __syncwarp();
+                    block(f + q * TB * NP, q + 1 < NB ? r0 + (q + 1) * TB * kCh : r1, q & 1, TB, Flag<true>{});
+                    yp += y_step;
                 }
-                before_y = ty + (size_t)(kTile - TB) * s.ys;
-                before_valid = TB;
-            } else {
+            } else {              // the first or the last tile of a request: blocks past its end change nothing
+                const int64_t skipped = (int64_t)(kTile - n) * s.ys;
 #pragma unroll 1
-                for (int j0 = 0; j0 < n; j0 += TB) {
-                    const Kept next = prepare(j0 + TB < n ? raw_row(buf, j0 + TB) : raw_row(buf1, 0), x ^ 1);
-                    advance(f + j0 * NP, x, n - j0, Flag<false>{});
-                    finish(before, x ^ 1, before_y, before_valid, Flag<false>{});
-                    before = now;
-                    now = next;
-                    before_y = ty + (size_t)j0 * s.ys;
-                    before_valid = min(TB, n - j0);
-                    x ^= 1;
-                    __syncwarp();
+                for (int q = 0; q < NB; ++q) {
+                    block(f + q * TB * NP, q + 1 < NB ? r0 + (q + 1) * TB * kCh : r1, q & 1, n - q * TB, Flag<false>{});
+                    yp += y_step;
                 }
+                float2 out[OWN];
+                finish(0, out, before, 1, yp, before_valid);
+                finish(1, out, before, 1, yp, before_valid);
+                before_valid = 0;
+                yp -= skipped;    // the next tile's rows follow the last that is there
             }
             buf = buf1;
             if (k + 1 < tiles) widen_bc(k + 1);
@@ -430,7 +459,9 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
                 }
             }
         }
-        finish(before, x ^ 1, before_y, before_valid, Flag<false>{});
+        float2 out[OWN];
+        finish(0, out, before, 1, yp, before_valid);
+        finish(1, out, before, 1, yp, before_valid);
     }
     if (io.final_states) put(io.final_states + (size_t)i * dn);
     if (io.final_slots) {
@@ -443,9 +474,9 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
     }
 }
 
-template <typename T, int NP, int L, bool kSoftplus, bool kGate>
+template <typename T, int NP, int L, bool kCommon>
 cudaError_t launch_g(const SelParams &p, cudaStream_t stream) {
-    constexpr auto kernel = selective_kernel<T, NP, L, kSoftplus, kGate>;
+    constexpr auto kernel = selective_kernel<T, NP, L, kCommon>;
     constexpr size_t smem = sizeof(typename Cfg<T, NP, L>::Smem);
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -456,8 +487,7 @@ cudaError_t launch_g(const SelParams &p, cudaStream_t stream) {
 
 template <typename T, int NP, int L>
 cudaError_t launch_k(const SelParams &p, cudaStream_t stream) {
-    if (p.s.softplus) return p.io.z ? launch_g<T, NP, L, true, true>(p, stream) : launch_g<T, NP, L, true, false>(p, stream);
-    return p.io.z ? launch_g<T, NP, L, false, true>(p, stream) : launch_g<T, NP, L, false, false>(p, stream);
+    return p.s.softplus && p.io.z && p.y_pair ? launch_g<T, NP, L, true>(p, stream) : launch_g<T, NP, L, false>(p, stream);
 }
 
 #ifndef SEL_L16
