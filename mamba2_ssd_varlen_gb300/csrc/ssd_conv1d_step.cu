@@ -4,8 +4,13 @@
 //   y[t, c] = act(bias[c] + sum_k weight[c, k] xin[t - (W-1) + k, c])
 //   state after token t = xin[t - (W-2) .. t]
 //
-// A thread owns one channel of one request and slides the window over its tokens.
+// Bound by memory and, at serving sizes, by the launch.  A thread owns kN neighbouring
+// channels, 16 bytes of a row of x: a slot's W-1 inputs a channel are then kN (W-1)
+// neighbouring elements, W-1 16-byte vectors, which move between their order in the slot
+// (channel by channel) and the window (input by input) in registers.  kN = 1 where rows,
+// slots or the width do not start on 16-byte boundaries.
 #include "pdl.cuh"
+#include "special.cuh"
 #include "ssd_internal.cuh"
 
 namespace ssd {
@@ -15,16 +20,42 @@ constexpr int kCsThreads = 128;
 
 struct ConvStepParams {
     int64_t T;
-    int32_t R, D, num_slots, silu;
+    int32_t R, D, num_slots, silu, tiles;
     const int32_t *cu;
     ssd_conv_io io;
 };
 
-template <typename T, int W>
+// kN raw elements, moved as one vector where kN elements are 16 bytes.
+template <typename T, int kN>
+struct Raw {
+    T v[kN];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (kN * sizeof(T) == 16) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(p);
+            memcpy(v, &q, 16);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kN; ++e) v[e] = p[e];
+        }
+    }
+    __device__ __forceinline__ void store(T *p) const {
+        if constexpr (kN * sizeof(T) == 16) {
+            uint4 q;
+            memcpy(&q, v, 16);
+            *reinterpret_cast<uint4 *>(p) = q;
+        } else {
+#pragma unroll
+            for (int e = 0; e < kN; ++e) p[e] = v[e];
+        }
+    }
+};
+
+template <typename T, int W, int kN>
 __global__ void __launch_bounds__(kCsThreads) conv1d_step_kernel(const __grid_constant__ ConvStepParams p) {
     pdl_wait();
     const ssd_conv_io &io = p.io;
-    const int i = blockIdx.y, c = blockIdx.x * kCsThreads + threadIdx.x;
+    const int i = (int)(blockIdx.x / p.tiles);
+    const int c = ((int)(blockIdx.x % p.tiles) * kCsThreads + (int)threadIdx.x) * kN;
     const int64_t a = p.cu[i], b = p.cu[i + 1];
     if (b < a || a < 0 || b > p.T || (i == 0 && a != 0) || (i == p.R - 1 && b != p.T)) {
         if (c == 0) atomicOr(io.device_err, SSD_DEVERR_CU_SEQLENS);
@@ -36,44 +67,90 @@ __global__ void __launch_bounds__(kCsThreads) conv1d_step_kernel(const __grid_co
     const size_t slot = (size_t)p.D * (W - 1), off = (size_t)c * (W - 1);
     const int rs = io.read_slots ? io.read_slots[i] : -1;
     if (rs >= p.num_slots && c == 0) atomicOr(io.device_err, SSD_DEVERR_INIT_SLOT);
-    T win[W];
-    float w[W];
+    Raw<T, kN> state[W - 1], in;  // the slot's order: element e (W-1) + k is input k of channel e
+    const bool held = rs >= 0 && rs < p.num_slots;
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
-        w[k] = io.weight[(size_t)c * W + k];
-        if (k < W - 1) win[k] = rs >= 0 && rs < p.num_slots ? pool[rs * slot + off + k] : from_f32<T>(0.f);
+    for (int k = 0; k < W - 1; ++k) {
+        if (held) {
+            state[k].load(pool + rs * slot + off + k * kN);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kN; ++e) state[k].v[e] = from_f32<T>(0.f);
+        }
     }
-    const float bias = io.bias ? io.bias[c] : 0.f;
+    in.load(x + (size_t)a * p.D);
+    float w[kN * W], bias[kN];
+    if constexpr (kN % 4 == 0) {
+#pragma unroll
+        for (int e = 0; e < kN * W; e += 4)
+            *reinterpret_cast<float4 *>(w + e) = *reinterpret_cast<const float4 *>(io.weight + (size_t)c * W + e);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kN * W; ++e) w[e] = io.weight[(size_t)c * W + e];
+    }
+#pragma unroll
+    for (int e = 0; e < kN; ++e) bias[e] = io.bias ? io.bias[c + e] : 0.f;
+    T win[W][kN];
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+        for (int e = 0; e < kN; ++e) win[k][e] = state[(e * (W - 1) + k) / kN].v[(e * (W - 1) + k) % kN];
     for (int64_t t = a; t < b; ++t) {
-        win[W - 1] = x[(size_t)t * p.D];
-        float v = bias;
-#pragma unroll
-        for (int k = 0; k < W; ++k) v = fmaf(w[k], to_f32(win[k]), v);
-        y[(size_t)t * p.D] = from_f32<T>(p.silu ? silu_f32(v) : v);
-#pragma unroll
-        for (int k = 0; k < W - 1; ++k) win[k] = win[k + 1];
         const int ws = io.write_slots ? io.write_slots[t] : -1;
+#pragma unroll
+        for (int e = 0; e < kN; ++e) win[W - 1][e] = in.v[e];
+        if (t + 1 < b) in.load(x + (size_t)(t + 1) * p.D);
+        Raw<T, kN> out;
+#pragma unroll
+        for (int e = 0; e < kN; ++e) {
+            float v = bias[e];
+#pragma unroll
+            for (int k = 0; k < W; ++k) v = fmaf(w[e * W + k], to_f32(win[k][e]), v);
+            out.v[e] = from_f32<T>(p.silu ? silu_sfu(v) : v);
+        }
+        out.store(y + (size_t)t * p.D);
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+            for (int e = 0; e < kN; ++e) win[k][e] = win[k + 1][e];
         if (ws >= p.num_slots) {
             if (c == 0) atomicOr(io.device_err, SSD_DEVERR_FINAL_SLOT);
         } else if (ws >= 0) {
 #pragma unroll
-            for (int k = 0; k < W - 1; ++k) pool[ws * slot + off + k] = win[k];
+            for (int k = 0; k < W - 1; ++k) {
+                Raw<T, kN> q;
+#pragma unroll
+                for (int e = 0; e < kN; ++e) q.v[e] = win[(k * kN + e) % (W - 1)][(k * kN + e) / (W - 1)];
+                q.store(pool + ws * slot + off + k * kN);
+            }
         }
     }
 }
 
-template <typename T>
-cudaError_t launch_cs(const ConvStepParams &p, int W, cudaStream_t stream) {
-    const dim3 grid((unsigned)((p.D + kCsThreads - 1) / kCsThreads), (unsigned)p.R), block(kCsThreads);
-    switch (W) {
-        case 2: return launch_after_prev(conv1d_step_kernel<T, 2>, grid, block, 0, stream, p);
-        case 3: return launch_after_prev(conv1d_step_kernel<T, 3>, grid, block, 0, stream, p);
-        case 4: return launch_after_prev(conv1d_step_kernel<T, 4>, grid, block, 0, stream, p);
-        default: return cudaErrorInvalidValue;
-    }
+template <typename T, int W>
+cudaError_t launch_cs_w(ConvStepParams &p, bool vec, cudaStream_t stream) {
+    constexpr int kN = 16 / sizeof(T);
+    const int per = kCsThreads * (vec ? kN : 1);
+    p.tiles = (p.D + per - 1) / per;
+    if ((int64_t)p.tiles * p.R > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)((int64_t)p.tiles * p.R)), block(kCsThreads);
+    return vec ? launch_after_prev(conv1d_step_kernel<T, W, kN>, grid, block, 0, stream, p)
+               : launch_after_prev(conv1d_step_kernel<T, W, 1>, grid, block, 0, stream, p);
 }
 
 bool aligned_to(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+template <typename T>
+cudaError_t launch_cs(ConvStepParams &p, int W, cudaStream_t stream) {
+    const bool vec = p.D % (16 / (int)sizeof(T)) == 0 && aligned_to(p.io.x, 16) && aligned_to(p.io.y, 16) &&
+                     aligned_to(p.io.conv_pool, 16) && aligned_to(p.io.weight, 16);
+    switch (W) {
+        case 2: return launch_cs_w<T, 2>(p, vec, stream);
+        case 3: return launch_cs_w<T, 3>(p, vec, stream);
+        case 4: return launch_cs_w<T, 4>(p, vec, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
 
 }  // namespace
 }  // namespace ssd
@@ -83,7 +160,7 @@ using namespace ssd;
 extern "C" int ssd_varlen_conv1d_step(const ssd_conv_dims *d, const int32_t *cu_seqlens, const ssd_conv_io *io,
                                       cudaStream_t stream) {
     if (!d || !cu_seqlens || !io) return SSD_ERR_NULL;
-    if (d->T < 0 || d->T > 0x7fffffffLL || d->R < 1 || d->R > 65535 || d->D < 1 || d->D > (1 << 24) ||
+    if (d->T < 0 || d->T > 0x7fffffffLL || d->R < 1 || d->D < 1 || d->D > (1 << 24) ||
         d->num_slots < 0)
         return SSD_ERR_DIMS;
     if (d->dtype != SSD_DTYPE_BF16 && d->dtype != SSD_DTYPE_F32) return SSD_ERR_DTYPE;

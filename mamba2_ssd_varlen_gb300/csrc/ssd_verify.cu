@@ -1,18 +1,33 @@
 // ssd_verify.cu -- verification of drafted tokens against the target's
 // probabilities from given random numbers (speculative sampling).
 //
-// One CTA per window.  Thread 0 counts the accepted drafts; the CTA then draws
-// the token that follows from one row's weights, held as whole multiples of
-// 2^-40 so that their sums do not depend on the order: each thread sums a run of
-// consecutive vocabulary entries, a scan over the threads finds the run that
-// holds the mark, and its thread walks that run.
+//   draft x of row t is accepted when accept_u q[x] < p[x]; the first that is not ends it,
+//   and the token that follows is drawn from that row's max(p - q, 0) (from p when every
+//   draft was accepted) by inversion, with weights f_v = floor(2^40 w_v).
+//
+// The sums are of whole numbers, so no order of adding changes the token: a window's
+// vocabulary is split over a cluster of S CTAs, whose totals meet in distributed shared
+// memory, and inside a CTA over warps by chunks of 1024 entries.  One pass reads the row (or
+// the two rows) and keeps a sum for every chunk; the chunk that holds the mark is then read
+// again by one warp.  A weight is added as two 20-bit digits in 32-bit registers: with w in
+// [0, 1], fma.rz(w, 2^20, 2^23) holds floor(2^20 w) in its mantissa, and the remainder gives
+// the second digit the same way, so that no conversion instruction is needed.
+//
+// Bound by memory: one row of V probabilities for a window whose drafts were all accepted,
+// two after a rejection, and a few gathered entries.
+#include <cooperative_groups.h>
+
 #include "pdl.cuh"
 #include "ssd_internal.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace ssd {
 namespace {
 
-constexpr int kVerThreads = 256;
+constexpr int kVerThreads = 512;
+constexpr int kChunk = 1024;     // vocabulary entries of a warp's chunk
+constexpr int kMaxCluster = 8;   // the portable limit
 
 struct VerifyParams {
     int64_t T, ts, qs;
@@ -21,96 +36,273 @@ struct VerifyParams {
     ssd_verify_io io;
 };
 
-// floor(2^40 min(max(w, 0), 1)), 0 for a NaN.  2^40 w is exact in fp32.
-__device__ __forceinline__ uint64_t fixed_weight(float w) {
-    return w > 0.f ? (uint64_t)__float2ull_rz(fminf(w, 1.f) * 1099511627776.f) : 0ull;
+// Sums of weights as two 20-bit digits; each term adds the bits of a float in [2^23, 2^24),
+// whose bias is taken off at the end (arithmetic modulo 2^32: up to 2^12 terms).
+struct Digits {
+    uint32_t hi = 0, lo = 0;
+    __device__ __forceinline__ void add(float w) {
+        w = fminf(fmaxf(w, 0.f), 1.f);  // a NaN counts as 0
+        const float t = __fmaf_rz(w, 1048576.f, 8388608.f);
+        const float rem = fmaf(w, 1048576.f, 8388608.f - t);  // exact
+        const float u = __fmaf_rz(rem, 1048576.f, 8388608.f);
+        hi += __float_as_uint(t);
+        lo += __float_as_uint(u);
+    }
+    __device__ __forceinline__ uint64_t total(uint32_t terms) const {
+        const uint32_t bias = terms * 0x4B000000u;
+        return ((uint64_t)(hi - bias) << 20) + (uint64_t)(lo - bias);
+    }
+};
+
+__device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
 
+// kVec neighbouring probabilities: one 16-byte load, or one element.
+template <typename T, int kVec>
+__device__ __forceinline__ void load_probs(const T *p, float (&v)[kVec]) {
+    if constexpr (kVec == 1) {
+        v[0] = to_f32(p[0]);
+    } else if constexpr (sizeof(T) == 4) {
+        const float4 q = *reinterpret_cast<const float4 *>(p);
+        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+    } else {
+        const uint4 q = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(w[e] << 16);
+            v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+        }
+    }
+}
+
+// A row's weights: the target's, less the draft's after a rejection (1 at the drafted token
+// where drafts have no distribution).
 template <typename T>
+struct Row {
+    const T *p, *q;  // q: NULL where nothing is taken off entry by entry
+    int drafted;     // the token that 1 is taken off, or -1
+};
+
+// kVec weights from entry v on, zeros past V.
+template <typename T, int kVec>
+__device__ __forceinline__ void load_weights(const Row<T> &row, int v, int V, float (&w)[kVec]) {
+    if (v + kVec <= V) {
+        load_probs<T, kVec>(row.p + v, w);
+        if (row.q) {
+            float q[kVec];
+            load_probs<T, kVec>(row.q + v, q);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) w[e] -= q[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            w[e] = v + e < V ? to_f32(row.p[v + e]) : 0.f;
+            if (row.q && v + e < V) w[e] -= to_f32(row.q[v + e]);
+        }
+    }
+    if ((unsigned)(row.drafted - v) < (unsigned)kVec) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+            if (v + e == row.drafted) w[e] -= 1.f;
+    }
+}
+
+template <typename T, int kVec>
 __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_constant__ VerifyParams p) {
+    constexpr int kWarps = kVerThreads / 32, kLoads = kChunk / (32 * kVec);
+    extern __shared__ unsigned long long chunk_sum[];  // of this CTA's chunks
+    __shared__ unsigned long long s_total;
+    __shared__ int s_n;
     pdl_wait();
+    cg::cluster_group cluster = cg::this_cluster();
+    const unsigned S = cluster.num_blocks(), rank = cluster.block_rank();
     const ssd_verify_io &io = p.io;
-    const int i = blockIdx.x, tid = threadIdx.x;
-    const int64_t a = p.cu[i], b = p.cu[i + 1];
+    const int i = (int)(blockIdx.x / S), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t a = p.cu[i], b = p.cu[i + 1];  // the same for the whole cluster, and so every return below
     if (b < a || a < 0 || b > p.T || (i == 0 && a != 0) || (i == p.R - 1 && b != p.T)) {
-        if (tid == 0) atomicOr(io.device_err, SSD_DEVERR_CU_SEQLENS);
+        if (rank == 0 && tid == 0) atomicOr(io.device_err, SSD_DEVERR_CU_SEQLENS);
         return;
     }
     if (a == b) {
-        if (tid == 0) io.accepted[i] = -1;
+        if (rank == 0 && tid == 0) io.accepted[i] = -1;
         return;
     }
-    __shared__ int s_n, s_pick;
-    __shared__ unsigned long long part[kVerThreads + 1];
     const T *P = static_cast<const T *>(io.target), *Q = static_cast<const T *>(io.draft);
     const int k = (int)(b - a - 1);
-    if (tid == 0) {
-        int n = 0;
-        for (; n < k; ++n) {
-            const int64_t t = a + n;
-            const int x = io.tokens[t + 1];
-            if (x < 0 || x >= p.V) {
-                atomicOr(io.device_err, SSD_DEVERR_TOKEN);
+    if (warp == 0) {  // the first draft that is not accepted, 32 at a time
+        int n = k;
+        for (int j0 = 0; j0 < k; j0 += 32) {
+            bool ok = true;
+            if (j0 + lane < k) {
+                const int64_t t = a + j0 + lane;
+                const int x = io.tokens[t + 1];
+                ok = x >= 0 && x < p.V;
+                if (ok) {
+                    const float q = Q ? to_f32(Q[t * p.qs + x]) : 1.f;
+                    ok = io.accept_u[t + 1] * q < to_f32(P[t * p.ts + x]);
+                }
+            }
+            const unsigned bad = __ballot_sync(0xffffffffu, !ok);
+            if (bad) {
+                n = j0 + __ffs(bad) - 1;
                 break;
             }
-            const float q = Q ? to_f32(Q[t * p.qs + x]) : 1.f;
-            if (!(io.accept_u[t + 1] * q < to_f32(P[t * p.ts + x]))) break;
         }
-        s_n = n;
-        s_pick = -1;
+        if (lane == 0) s_n = n;
     }
     __syncthreads();
     const int n = s_n;
     const int64_t r = a + n;
-    const T *pr = P + r * p.ts;
+    Row<T> row{P + r * p.ts, nullptr, -1};
     bool residual = n < k;
-    const int drafted = residual ? io.tokens[r + 1] : -1;
-    auto weight = [&](int v) -> uint64_t {
-        float w = to_f32(pr[v]);
-        if (residual) {
-            if (Q) w -= to_f32(Q[r * p.qs + v]);
-            else if (v == drafted) w -= 1.f;
-        }
-        return fixed_weight(w);
-    };
-    const int run = (p.V + kVerThreads - 1) / kVerThreads;
-    const int lo = min(tid * run, p.V), hi = min(lo + run, p.V);
-    unsigned long long total = 0;
+    if (residual) {
+        const int x = io.tokens[r + 1];
+        if (rank == 0 && tid == 0 && (x < 0 || x >= p.V)) atomicOr(io.device_err, SSD_DEVERR_TOKEN);
+        if (Q) row.q = Q + r * p.qs;
+        else row.drafted = x;
+    }
+    const int chunks = (p.V + kChunk - 1) / kChunk;
+    const int c0 = (int)((int64_t)rank * chunks / S), c1 = (int)((int64_t)(rank + 1) * chunks / S);
+
+    unsigned long long before = 0, total = 0;  // of the CTAs before this one, of the row
     for (;;) {
-        uint64_t sum = 0;
-        for (int v = lo; v < hi; ++v) sum += weight(v);
-        part[tid + 1] = sum;
-        if (tid == 0) part[0] = 0;
+        unsigned long long mine = 0;
+        for (int c = c0 + warp; c < c1; c += kWarps) {
+            Digits d;
+            const int v0 = c * kChunk + lane * kVec;
+#pragma unroll 8
+            for (int e = 0; e < kLoads; ++e) {
+                float w[kVec];
+                load_weights<T, kVec>(row, v0 + e * 32 * kVec, p.V, w);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) d.add(w[j]);
+            }
+            const uint64_t sum = warp_sum(d.total(kLoads * kVec));
+            if (lane == 0) chunk_sum[c - c0] = sum;
+            mine += sum;
+        }
+        if (tid == 0) s_total = 0;
         __syncthreads();
-        if (tid == 0)
-            for (int j = 1; j <= kVerThreads; ++j) part[j] += part[j - 1];
-        __syncthreads();
-        total = part[kVerThreads];
+        if (lane == 0 && mine) atomicAdd(&s_total, mine);  // whole numbers: any order
+        cluster.sync();
+        before = total = 0;
+        for (unsigned q = 0; q < S; ++q) {
+            const unsigned long long v = *cluster.map_shared_rank(&s_total, q);
+            if (q < rank) before += v;
+            total += v;
+        }
+        cluster.sync();  // nobody's total is read any more: it may be rewritten, and CTAs may end
         if (total != 0 || !residual) break;
         residual = false;  // no weight is positive after a rejection: the target's own
-        __syncthreads();
+        row.q = nullptr;
+        row.drafted = -1;
     }
-    if (total != 0) {
-        const double f = (double)io.sample_u[i] * (double)total;
-        unsigned long long mark = f >= 1.0 ? (unsigned long long)f : 0ull;  // also for a NaN
-        mark = min(mark, total - 1);
-        if (part[tid] <= mark && mark < part[tid + 1]) {
-            unsigned long long c = part[tid];
-            int v = lo;
-            for (;; ++v) {
-                c += weight(v);
-                if (c > mark) break;
-            }
-            s_pick = v;
+
+    if (rank == 0) {
+        for (int64_t j = tid; j < b - a; j += kVerThreads)
+            if (j != n || total == 0) io.out_tokens[a + j] = j < n ? io.tokens[a + j + 1] : -1;
+        if (tid == 0) {
+            io.accepted[i] = n;
+            if (io.next_slots) io.next_slots[i] = io.write_slots[r];
         }
     }
-    __syncthreads();
-    for (int j = tid; j < b - a; j += kVerThreads)
-        io.out_tokens[a + j] = j < n ? io.tokens[a + j + 1] : j == n ? s_pick : -1;
-    if (tid == 0) {
-        io.accepted[i] = n;
-        if (io.next_slots) io.next_slots[i] = io.write_slots[r];
+    if (warp != 0 || total == 0) return;
+    const double f = (double)io.sample_u[i] * (double)total;
+    unsigned long long mark = f >= 1.0 ? (unsigned long long)f : 0ull;  // 0 for a NaN too
+    mark = min(mark, total - 1);
+    if (mark < before) return;
+    mark -= before;  // among this CTA's own chunks, if there at all
+    // the first chunk, then the first entry, whose running sum is over the mark
+    auto scan = [&](unsigned long long v) {  // inclusive over the lanes
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long w = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += w;
+        }
+        return v;
+    };
+    int hit = -1;
+    for (int c = 0; c < c1 - c0 && hit < 0; c += 32) {
+        const unsigned long long run = scan(c + lane < c1 - c0 ? chunk_sum[c + lane] : 0ull);
+        const unsigned over = __ballot_sync(0xffffffffu, run > mark);
+        if (over) {
+            const int l = __ffs(over) - 1;
+            const unsigned long long below = l ? __shfl_sync(0xffffffffu, run, l - 1) : 0ull;
+            hit = c + l;
+            mark -= below;
+        } else {
+            mark -= __shfl_sync(0xffffffffu, run, 31);
+        }
     }
+    if (hit < 0) return;  // a later CTA's
+#pragma unroll 1
+    for (int e = 0; e < kLoads; ++e) {
+        const int v0 = (c0 + hit) * kChunk + (e * 32 + lane) * kVec;
+        float w[kVec];
+        load_weights<T, kVec>(row, v0, p.V, w);
+        uint64_t each[kVec], sum = 0;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            Digits d;
+            d.add(w[j]);
+            sum += each[j] = d.total(1);
+        }
+        const unsigned long long run = scan(sum);
+        const unsigned over = __ballot_sync(0xffffffffu, run > mark);
+        if (over) {
+            if (lane == __ffs(over) - 1) {
+                unsigned long long c = run - sum;
+                int v = v0;
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    c += each[j];
+                    v += c <= mark;
+                }
+                io.out_tokens[r] = v;
+            }
+            return;
+        }
+        mark -= __shfl_sync(0xffffffffu, run, 31);
+    }
+}
+
+template <typename T, int kVec>
+cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream) {
+    const int chunks = (p.V + kChunk - 1) / kChunk;
+    // CTAs a window: enough for two on every SM, but at least a chunk for each of a CTA's warps, so that few
+    // windows spread over the GPU and many do not pay for a cluster's barriers.
+    int S = 1;
+    while (S < kMaxCluster && (int64_t)p.R * S < 2 * 152 && chunks >= 2 * S * (kVerThreads / 32)) S *= 2;
+    const size_t smem = (size_t)((chunks + S - 1) / S + 1) * sizeof(unsigned long long);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = S;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.R * S));
+    cfg.blockDim = dim3(kVerThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, verify_kernel<T, kVec>, p);
+}
+
+template <typename T>
+cudaError_t launch_verify_t(const VerifyParams &p, cudaStream_t stream) {
+    auto rows16 = [](const void *ptr, int64_t stride) {
+        return ((uintptr_t)ptr & 15) == 0 && stride * sizeof(T) % 16 == 0;
+    };
+    if (rows16(p.io.target, p.ts) && (!p.io.draft || rows16(p.io.draft, p.qs)))
+        return launch_verify<T, 16 / sizeof(T)>(p, stream);
+    return launch_verify<T, 1>(p, stream);
 }
 
 }  // namespace
@@ -146,9 +338,7 @@ extern "C" int ssd_varlen_verify(const ssd_verify_dims *d, const int32_t *cu_seq
     p.qs = qs;
     p.cu = cu_seqlens;
     p.io = *io;
-    const dim3 grid((unsigned)d->R), block(kVerThreads);
-    const cudaError_t err = d->dtype == SSD_DTYPE_BF16
-                                ? launch_after_prev(verify_kernel<__nv_bfloat16>, grid, block, 0, stream, p)
-                                : launch_after_prev(verify_kernel<float>, grid, block, 0, stream, p);
+    const cudaError_t err = d->dtype == SSD_DTYPE_BF16 ? launch_verify_t<__nv_bfloat16>(p, stream)
+                                                       : launch_verify_t<float>(p, stream);
     return err == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
