@@ -614,7 +614,31 @@ def _selective_dims(prob, num_slots, block_size=0, block_table_width=0):
                               row("delta", (D,)), row("B", (G, N)), row("C", (G, N)), row("z", (D,)), 0)
 
 
-class SelectiveScanCall:
+class _Prepared:
+    """What the call handles below share: the prepared C call (function, dims, cu_seqlens, io), the device error word."""
+
+    def _prepare(self, name):
+        fn = getattr(load_library(), name)
+        cu = self.prob["cu_seqlens"]
+        import torch
+        _check_plain(cu, (self.dims.R + 1,), torch.int32, "cu_seqlens")
+        self._name, self._fn = name, fn
+        self._args = (ctypes.byref(self.dims), _ptr(cu), ctypes.byref(self.io))
+
+    def __call__(self):
+        rc = self._fn(*self._args, _stream(self.stream))
+        if rc != 0:
+            raise SsdError(rc, self._name)
+        return self
+
+    def status(self) -> int:
+        """Device error bits of the calls so far (synchronises), then clears them."""
+        v = int(self.err[0].item())
+        self.err.zero_()
+        return v
+
+
+class SelectiveScanCall(_Prepared):
     """One selective-scan prefill over a problem from workloads.make_selective_problem: outputs (y,
     final_states), the device error word, the workspace, and the pre-built argument structs."""
 
@@ -639,16 +663,7 @@ class SelectiveScanCall:
                                    _ptr(prob.get("final_slots")), _ptr(bt), _ptr(self.y), _ptr(self.final_states),
                                    _ptr(self.workspace), need, _ptr(self.err))
         self.stream = stream
-
-    def __call__(self):
-        ssd_varlen_selective_scan(self.dims, self.prob["cu_seqlens"], self.io, self.stream)
-        return self
-
-    def status(self) -> int:
-        """Device error bits of the calls so far (synchronises), then clears them."""
-        v = int(self.err[0].item())
-        self.err.zero_()
-        return v
+        self._prepare("ssd_varlen_selective_scan")
 
 
 def run_selective_scan(prob: dict, **kw) -> SelectiveScanCall:
@@ -656,7 +671,7 @@ def run_selective_scan(prob: dict, **kw) -> SelectiveScanCall:
     return SelectiveScanCall(prob, **kw)()
 
 
-class SelectiveStepCall:
+class SelectiveStepCall(_Prepared):
     """One selective-scan step over decode or speculative windows (workloads.make_selective_step_problem):
     the output y, the device error word, and the pre-built argument structs; the pool is updated."""
 
@@ -673,15 +688,7 @@ class SelectiveStepCall:
                                         _ptr(pool), _ptr(prob["read_slots"]), _ptr(prob.get("write_slots")),
                                         _ptr(self.y), _ptr(self.err))
         self.stream = stream
-
-    def __call__(self):
-        ssd_varlen_selective_step(self.dims, self.prob["cu_seqlens"], self.io, self.stream)
-        return self
-
-    def status(self) -> int:
-        v = int(self.err[0].item())
-        self.err.zero_()
-        return v
+        self._prepare("ssd_varlen_selective_step")
 
 
 def run_selective_step(prob: dict, **kw) -> SelectiveStepCall:
@@ -689,13 +696,13 @@ def run_selective_step(prob: dict, **kw) -> SelectiveStepCall:
     return SelectiveStepCall(prob, **kw)()
 
 
-class ConvStepCall(Conv1dCall):
+class ConvStepCall(_Prepared, Conv1dCall):
     """One causal conv1d step over decode or speculative windows: a Conv1dCall whose write_slots has a slot
     for every token (and whose D may be any)."""
 
-    def __call__(self):
-        ssd_varlen_conv1d_step(self.dims, self.prob["cu_seqlens"], self.io, self.stream)
-        return self
+    def __init__(self, prob: dict, stream=None):
+        Conv1dCall.__init__(self, prob, stream)
+        self._prepare("ssd_varlen_conv1d_step")
 
 
 def run_conv1d_step(prob: dict, **kw) -> ConvStepCall:
@@ -703,7 +710,7 @@ def run_conv1d_step(prob: dict, **kw) -> ConvStepCall:
     return ConvStepCall(prob, **kw)()
 
 
-class VerifyCall:
+class VerifyCall(_Prepared):
     """One verification of drafted tokens (workloads.make_verify_problem): outputs (accepted, out_tokens,
     next_slots where write_slots is given), the device error word, and the pre-built argument structs."""
 
@@ -734,15 +741,7 @@ class VerifyCall:
                                 _ptr(prob["sample_u"]), _ptr(slots), _ptr(self.accepted), _ptr(self.out_tokens),
                                 _ptr(self.next_slots), _ptr(self.err))
         self.stream = stream
-
-    def __call__(self):
-        ssd_varlen_verify(self.dims, self.prob["cu_seqlens"], self.io, self.stream)
-        return self
-
-    def status(self) -> int:
-        v = int(self.err[0].item())
-        self.err.zero_()
-        return v
+        self._prepare("ssd_varlen_verify")
 
 
 def run_verify(prob: dict, **kw) -> VerifyCall:

@@ -9,7 +9,10 @@
 // neighbouring elements, W-1 16-byte vectors, which move between their order in the slot
 // (channel by channel) and the window (input by input) in registers.  kN = 1 where rows,
 // slots or the width do not start on 16-byte boundaries.
+#include <algorithm>
+
 #include "pdl.cuh"
+#include "resident.cuh"
 #include "special.cuh"
 #include "ssd_internal.cuh"
 
@@ -20,7 +23,7 @@ constexpr int kCsThreads = 128;
 
 struct ConvStepParams {
     int64_t T;
-    int32_t R, D, num_slots, silu, tiles;
+    int32_t R, D, num_slots, silu, tiles, rb;
     const int32_t *cu;
     ssd_conv_io io;
 };
@@ -54,88 +57,118 @@ template <typename T, int W, int kN>
 __global__ void __launch_bounds__(kCsThreads) conv1d_step_kernel(const __grid_constant__ ConvStepParams p) {
     pdl_wait();
     const ssd_conv_io &io = p.io;
-    const int i = (int)(blockIdx.x / p.tiles);
+    const int lane = threadIdx.x & 31;
+    const int i0 = (int)(blockIdx.x / p.tiles) * p.rb, count = min(p.rb, p.R - i0);
     const int c = ((int)(blockIdx.x % p.tiles) * kCsThreads + (int)threadIdx.x) * kN;
-    const int64_t a = p.cu[i], b = p.cu[i + 1];
-    if (b < a || a < 0 || b > p.T || (i == 0 && a != 0) || (i == p.R - 1 && b != p.T)) {
-        if (c == 0) atomicOr(io.device_err, SSD_DEVERR_CU_SEQLENS);
-        return;
+    const bool there = c < p.D;
+    // lane q: the window and the read slot of request i0 + q
+    int ma = 0, mb = 0, ms = -1;
+    if (lane < count) {
+        const int i = i0 + lane;
+        ma = p.cu[i], mb = p.cu[i + 1];
+        if (mb < ma || ma < 0 || mb > p.T || (i == 0 && ma != 0) || (i == p.R - 1 && mb != p.T)) {
+            if (blockIdx.x % p.tiles == 0) atomicOr(io.device_err, SSD_DEVERR_CU_SEQLENS);
+            ma = mb = 0;
+        }
+        if (mb > ma && io.read_slots) ms = io.read_slots[i];
+        if (ms >= p.num_slots) {
+            if (blockIdx.x % p.tiles == 0) atomicOr(io.device_err, SSD_DEVERR_INIT_SLOT);
+            ms = -1;
+        }
     }
-    if (c >= p.D || a == b) return;
     const T *x = static_cast<const T *>(io.x) + c;
     T *pool = static_cast<T *>(io.conv_pool), *y = static_cast<T *>(io.y) + c;
     const size_t slot = (size_t)p.D * (W - 1), off = (size_t)c * (W - 1);
-    const int rs = io.read_slots ? io.read_slots[i] : -1;
-    if (rs >= p.num_slots && c == 0) atomicOr(io.device_err, SSD_DEVERR_INIT_SLOT);
     Raw<T, kN> state[W - 1], in;  // the slot's order: element e (W-1) + k is input k of channel e
-    const bool held = rs >= 0 && rs < p.num_slots;
+    auto fetch = [&](int q) {     // the state and the first input of request i0 + q
+        const int rs = __shfl_sync(0xffffffffu, ms, q), a = __shfl_sync(0xffffffffu, ma, q);
+        const int b = __shfl_sync(0xffffffffu, mb, q);
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) {
-        if (held) {
-            state[k].load(pool + rs * slot + off + k * kN);
-        } else {
+        for (int k = 0; k < W - 1; ++k) {
+            if (rs >= 0 && there) {
+                state[k].load(pool + rs * slot + off + k * kN);
+            } else {
 #pragma unroll
-            for (int e = 0; e < kN; ++e) state[k].v[e] = from_f32<T>(0.f);
+                for (int e = 0; e < kN; ++e) state[k].v[e] = from_f32<T>(0.f);
+            }
         }
-    }
-    in.load(x + (size_t)a * p.D);
+        if (b > a && there) in.load(x + (size_t)a * p.D);
+    };
+    fetch(0);
     float w[kN * W], bias[kN];
+#pragma unroll
+    for (int e = 0; e < kN; ++e) bias[e] = there && io.bias ? io.bias[c + e] : 0.f;
     if constexpr (kN % 4 == 0) {
 #pragma unroll
         for (int e = 0; e < kN * W; e += 4)
-            *reinterpret_cast<float4 *>(w + e) = *reinterpret_cast<const float4 *>(io.weight + (size_t)c * W + e);
+            *reinterpret_cast<float4 *>(w + e) = there ? *reinterpret_cast<const float4 *>(io.weight + (size_t)c * W + e)
+                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
     } else {
 #pragma unroll
-        for (int e = 0; e < kN * W; ++e) w[e] = io.weight[(size_t)c * W + e];
+        for (int e = 0; e < kN * W; ++e) w[e] = there ? io.weight[(size_t)c * W + e] : 0.f;
     }
-#pragma unroll
-    for (int e = 0; e < kN; ++e) bias[e] = io.bias ? io.bias[c + e] : 0.f;
-    T win[W][kN];
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-        for (int e = 0; e < kN; ++e) win[k][e] = state[(e * (W - 1) + k) / kN].v[(e * (W - 1) + k) % kN];
-    for (int64_t t = a; t < b; ++t) {
-        const int ws = io.write_slots ? io.write_slots[t] : -1;
-#pragma unroll
-        for (int e = 0; e < kN; ++e) win[W - 1][e] = in.v[e];
-        if (t + 1 < b) in.load(x + (size_t)(t + 1) * p.D);
-        Raw<T, kN> out;
-#pragma unroll
-        for (int e = 0; e < kN; ++e) {
-            float v = bias[e];
-#pragma unroll
-            for (int k = 0; k < W; ++k) v = fmaf(w[e * W + k], to_f32(win[k][e]), v);
-            out.v[e] = from_f32<T>(p.silu ? silu_sfu(v) : v);
-        }
-        out.store(y + (size_t)t * p.D);
+    for (int q = 0; q < count; ++q) {
+        const int a = __shfl_sync(0xffffffffu, ma, q), b = __shfl_sync(0xffffffffu, mb, q);
+        T win[W][kN];
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
 #pragma unroll
-            for (int e = 0; e < kN; ++e) win[k][e] = win[k + 1][e];
-        if (ws >= p.num_slots) {
-            if (c == 0) atomicOr(io.device_err, SSD_DEVERR_FINAL_SLOT);
-        } else if (ws >= 0) {
+            for (int e = 0; e < kN; ++e) win[k][e] = state[(e * (W - 1) + k) / kN].v[(e * (W - 1) + k) % kN];
 #pragma unroll
-            for (int k = 0; k < W - 1; ++k) {
-                Raw<T, kN> q;
+        for (int e = 0; e < kN; ++e) win[W - 1][e] = in.v[e];
+        if (q + 1 < count) fetch(q + 1);  // on its way while this window is computed
+        for (int t = a; t < b; ++t) {
+            const int ws = io.write_slots ? io.write_slots[t] : -1;
+            Raw<T, kN> ahead, out;
+            if (t + 1 < b && there) ahead.load(x + (size_t)(t + 1) * p.D);
 #pragma unroll
-                for (int e = 0; e < kN; ++e) q.v[e] = win[(k * kN + e) % (W - 1)][(k * kN + e) / (W - 1)];
-                q.store(pool + ws * slot + off + k * kN);
+            for (int e = 0; e < kN; ++e) {
+                float v = bias[e];
+#pragma unroll
+                for (int k = 0; k < W; ++k) v = fmaf(w[e * W + k], to_f32(win[k][e]), v);
+                out.v[e] = from_f32<T>(p.silu ? silu_sfu(v) : v);
+            }
+            if (there) out.store(y + (size_t)t * p.D);
+            if (ws >= p.num_slots) {
+                if (c == 0) atomicOr(io.device_err, SSD_DEVERR_FINAL_SLOT);
+            } else if (ws >= 0 && there) {
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k) {
+                    Raw<T, kN> s;
+#pragma unroll
+                    for (int e = 0; e < kN; ++e)
+                        s.v[e] = win[(k * kN + e) % (W - 1) + 1][(k * kN + e) / (W - 1)];
+                    s.store(pool + ws * slot + off + k * kN);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < kN; ++e) {
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k) win[k][e] = win[k + 1][e];
+                win[W - 1][e] = ahead.v[e];
             }
         }
     }
 }
 
+template <typename T, int W, int kN>
+cudaError_t launch_cs_n(ConvStepParams &p, cudaStream_t stream) {
+    constexpr auto kernel = conv1d_step_kernel<T, W, kN>;
+    static int64_t cached[kResidentDevices] = {};
+    int64_t resident = 0;
+    const cudaError_t e = resident_ctas_at(cached, kernel, kCsThreads, 0, resident);
+    if (e != cudaSuccess) return e;
+    p.tiles = (p.D + kCsThreads * kN - 1) / (kCsThreads * kN);
+    // requests a CTA, one after the other with the weights in registers: as many as leave one wave of resident CTAs
+    p.rb = (int)std::min<int64_t>(32, std::max<int64_t>(1, ((int64_t)p.tiles * p.R + resident - 1) / resident));
+    const int64_t ctas = (int64_t)p.tiles * ((p.R + p.rb - 1) / p.rb);
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    return launch_after_prev(kernel, dim3((unsigned)ctas), dim3(kCsThreads), 0, stream, p);
+}
+
 template <typename T, int W>
 cudaError_t launch_cs_w(ConvStepParams &p, bool vec, cudaStream_t stream) {
-    constexpr int kN = 16 / sizeof(T);
-    const int per = kCsThreads * (vec ? kN : 1);
-    p.tiles = (p.D + per - 1) / per;
-    if ((int64_t)p.tiles * p.R > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const dim3 grid((unsigned)((int64_t)p.tiles * p.R)), block(kCsThreads);
-    return vec ? launch_after_prev(conv1d_step_kernel<T, W, kN>, grid, block, 0, stream, p)
-               : launch_after_prev(conv1d_step_kernel<T, W, 1>, grid, block, 0, stream, p);
+    return vec ? launch_cs_n<T, W, 16 / sizeof(T)>(p, stream) : launch_cs_n<T, W, 1>(p, stream);
 }
 
 bool aligned_to(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }

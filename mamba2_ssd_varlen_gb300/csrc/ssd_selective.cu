@@ -19,6 +19,7 @@
 //     for different tokens, and exchanged through shared memory.  They, and the sums over
 //     the L lanes, belong to the blocks of TB tokens after and before the one whose
 //     recurrence runs beside them, so that their latency hides behind it.
+#include "async_copy.cuh"
 #include "pdl.cuh"
 #include "selective.cuh"
 #include "special.cuh"
@@ -42,18 +43,6 @@ struct SelParams {
     int32_t bc_vec;  // B, C: every four states of a row start on a boundary of four elements
     int32_t y_pair;  // y: every pair of channels starts on a boundary of two elements
 };
-
-__device__ __forceinline__ void cp16(void *smem, const void *gmem) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem)
-                 : "memory");
-}
-__device__ __forceinline__ void cp4(void *smem, const void *gmem) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kPending>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory"); }
 
 template <typename T>
 __device__ __forceinline__ void cp_elem(T *smem, const T *gmem) {

@@ -3,18 +3,33 @@
 //
 // Bound by the states: N fp32 values a channel read once a window and written once a
 // token.  QL lanes hold a channel, four neighbouring states each (one 16-byte access, the
-// lanes of a channel a whole run of sectors), and CPG channels a lane group, so that a lane
-// has CPG independent 16-byte loads in flight; each lane computes the step and the gate of
-// one of its group's channels and hands them round by shuffles.  Rows of u, delta, z and y
-// are read and written 32 neighbouring channels at a time.
+// lanes of a channel a whole run of sectors), and CPG channels a lane group; a warp takes
+// its channels through the windows of several requests one after the other, so that A is
+// read once for them.  The next requests' states are on their way meanwhile: every lane
+// copies what it will itself read into a ring of its own in shared memory (asynchronous
+// copies: bytes in flight cost no registers, and the ring needs no barrier).  Each lane
+// computes the step and the gate of one of its group's channels and hands them round by
+// shuffles; rows of u, delta, z and y are read and written 32 neighbouring channels at a
+// time, a token ahead.
+#include <algorithm>
+
+#include "async_copy.cuh"
 #include "pdl.cuh"
+#include "resident.cuh"
 #include "selective.cuh"
 #include "special.cuh"
 
 namespace ssd {
 namespace {
 
+#ifndef STEP_MIN
+#define STEP_MIN 5
+#endif
+#ifndef STEP_RING
+#define STEP_RING 3
+#endif
 constexpr int kStepThreads = 128;
+constexpr int kMaxRb = 32;        // requests of a warp: their slots sit in its lanes
 
 struct SelStepParams {
     SelShape s;
@@ -22,6 +37,7 @@ struct SelStepParams {
     ssd_selective_step_io io;
     int32_t vec;     // states: every four start on a 16-byte boundary
     int32_t bc_vec;  // B, C: every four start on a boundary of four elements
+    int32_t rb;      // requests a warp takes, one after the other
 };
 
 __device__ __forceinline__ float4 four(const float *p) { return *reinterpret_cast<const float4 *>(p); }
@@ -40,51 +56,86 @@ __device__ __forceinline__ float4 some(const T *p, int n) {
 
 // QL lanes a channel with 4 NV states each (quad v of a lane: states 4 (l + QL v) ..), CPG channels a lane group.
 template <typename T, int QL, int NV>
-__global__ void __launch_bounds__(kStepThreads) selective_step_kernel(const __grid_constant__ SelStepParams p) {
+__global__ void __launch_bounds__(kStepThreads, QL == 32 && NV == 2 ? 2 : STEP_MIN)
+    selective_step_kernel(const __grid_constant__ SelStepParams p) {
     constexpr int GR = 32 / QL;               // lane groups of a warp
     constexpr int CPG = QL < 4 ? QL : 4;      // channels of a group
     constexpr int CW = GR * CPG;              // channels of a warp
+    constexpr int kRing = NV == 1 ? STEP_RING : 2;  // requests whose states a lane holds or has on their way
+    __shared__ float4 ring[kRing][CPG][NV][kStepThreads];
     pdl_wait();
     const SelShape &s = p.s;
     const ssd_selective_step_io &io = p.io;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % QL, gr = lane / QL;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = lane % QL, gr = lane / QL;
     const int tiles = (s.D / s.G + CW - 1) / CW * s.G;  // of CW channels, none over two groups of B and C
+    const int blocks = (s.R + p.rb - 1) / p.rb;
     const int64_t item = (int64_t)blockIdx.x * (kStepThreads / 32) + warp;
-    if (item >= (int64_t)tiles * s.R) return;
-    const int i = (int)(item / tiles), tile = (int)(item % tiles);
+    if (item >= (int64_t)tiles * blocks) return;
+    const int i0 = (int)(item / tiles) * p.rb, count = min(p.rb, s.R - i0), tile = (int)(item % tiles);
     const int dg = s.D / s.G, per_group = tiles / s.G, g = tile / per_group;
     const int d0 = g * dg + tile % per_group * CW, width = min(CW, (g + 1) * dg - d0);
-    const bool first = tile == 0 && lane == 0;
-    const int64_t a = p.cu[i], b = p.cu[i + 1];
-    if (b < a || a < 0 || b > s.T || (i == 0 && a != 0) || (i == s.R - 1 && b != s.T)) {
-        if (first) atomicOr(io.device_err, SSD_DEVERR_CU_SEQLENS);
-        return;
-    }
-    if (a == b) return;
-    const int rs = io.read_slots[i];
-    if (rs >= s.num_slots && first) atomicOr(io.device_err, SSD_DEVERR_INIT_SLOT);
     const size_t dn = (size_t)s.D * s.N;
-    const float *src = rs >= 0 && rs < s.num_slots ? io.state_pool + (size_t)rs * dn : nullptr;
 
-    // channel k of the group: gr + GR k, so that a warp's access covers neighbouring channels
-    float4 h[CPG][NV], A[CPG][NV];
-#pragma unroll
-    for (int k = 0; k < CPG; ++k) {
-        const int ch = gr + GR * k;
-        const size_t row = (size_t)(d0 + ch) * s.N;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int n0 = 4 * (l + QL * v), n = ch < width ? min(4, s.N - n0) : 0;
-            const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (p.vec) {
-                h[k][v] = src && n > 0 ? four(src + row + n0) : zero;
-                A[k][v] = n > 0 ? four(io.A + row + n0) : zero;
-            } else {
-                h[k][v] = src ? some(src + row + n0, n) : zero;
-                A[k][v] = some(io.A + row + n0, n);
-            }
+    // lane q: the window and the read slot of request i0 + q
+    int ma = 0, mb = 0, ms = -1;
+    if (lane < count) {
+        const int i = i0 + lane;
+        ma = p.cu[i], mb = p.cu[i + 1];
+        if (mb < ma || ma < 0 || mb > s.T || (i == 0 && ma != 0) || (i == s.R - 1 && mb != s.T)) {
+            if (tile == 0) atomicOr(io.device_err, SSD_DEVERR_CU_SEQLENS);
+            ma = mb = 0;
+        }
+        if (mb > ma) ms = io.read_slots[i];
+        if (ms >= s.num_slots) {
+            if (tile == 0) atomicOr(io.device_err, SSD_DEVERR_INIT_SLOT);
+            ms = -1;
         }
     }
+    // channel k of the group: gr + GR k, so that a warp's access covers neighbouring channels
+    auto quad = [&](int k, int v, int &n) {  // first state of quad (k, v), and how many of it there are
+        const int ch = gr + GR * k, n0 = 4 * (l + QL * v);
+        n = ch < width ? min(4, s.N - n0) : 0;
+        return (size_t)(d0 + ch) * s.N + n0;
+    };
+    auto stage = [&](int q) {  // the states of request i0 + q, on their way
+        const int slot = q < count ? __shfl_sync(0xffffffffu, ms, q) : -1;
+        const float *src = io.state_pool + (size_t)max(slot, 0) * dn;
+#pragma unroll
+        for (int k = 0; k < CPG; ++k)
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                float4 *dst = &ring[q % kRing][k][v][tid];
+                int n;
+                const size_t at = quad(k, v, n);
+                if (slot < 0 || n <= 0) {
+                    *dst = make_float4(0.f, 0.f, 0.f, 0.f);
+                } else if (p.vec) {
+                    cp16(dst, src + at);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float *w = reinterpret_cast<float *>(dst) + e;
+                        if (e < n) cp4(w, src + at + e);
+                        else *w = 0.f;
+                    }
+                }
+            }
+        cp_commit();
+    };
+#pragma unroll
+    for (int q = 0; q < kRing - 1; ++q) stage(q);
+
+    float4 A[CPG][NV];
+#pragma unroll
+    for (int k = 0; k < CPG; ++k)
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            int n;
+            const size_t at = quad(k, v, n);
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (n > 0) x = p.vec ? four(io.A + at) : some(io.A + at, n);
+            A[k][v] = make_float4(x.x * kLog2e, x.y * kLog2e, x.z * kLog2e, x.w * kLog2e);
+        }
     // the lane's own channel (lanes past CPG have none)
     const int own = gr + GR * l, d = d0 + own;
     const bool mine = l < CPG && own < width;
@@ -93,117 +144,132 @@ __global__ void __launch_bounds__(kStepThreads) selective_step_kernel(const __gr
     const T *z = io.z ? static_cast<const T *>(io.z) + d : nullptr;
     const T *B = static_cast<const T *>(io.B) + (size_t)g * s.N, *C = static_cast<const T *>(io.C) + (size_t)g * s.N;
     T *y = static_cast<T *>(io.y) + d;
-#pragma unroll
-    for (int k = 0; k < CPG; ++k)
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            A[k][v].x *= kLog2e;
-            A[k][v].y *= kLog2e;
-            A[k][v].z *= kLog2e;
-            A[k][v].w *= kLog2e;
-        }
-    // the next token's inputs are fetched while this one's states move
-    float un = 0.f, dn1 = 0.f, zn = 0.f;
-    float4 bn[NV], cn[NV];
+
+    // a token's inputs, fetched while the one before it is computed
+    struct {
+        float u, dt, z;
+        int ws;
+        float4 b[NV], c[NV];
+    } in = {};
     auto fetch = [&](int64_t t) {
         if (mine) {
-            un = to_f32(u[t * s.us]);
-            dn1 = to_f32(dl[t * s.ds]);
-            if (z) zn = to_f32(z[t * s.zs]);
+            in.u = to_f32(u[t * s.us]);
+            in.dt = to_f32(dl[t * s.ds]);
+            if (z) in.z = to_f32(z[t * s.zs]);
         }
+        in.ws = io.write_slots ? io.write_slots[t] : -1;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int n0 = 4 * (l + QL * v), n = min(4, s.N - n0);
             const T *tb = B + t * s.bs + n0, *tc = C + t * s.cs + n0;
             if (p.bc_vec && n > 0) {
-                bn[v] = four(tb);
-                cn[v] = four(tc);
+                in.b[v] = four(tb);
+                in.c[v] = four(tc);
             } else {
-                bn[v] = some(tb, n);
-                cn[v] = some(tc, n);
+                in.b[v] = some(tb, n);
+                in.c[v] = some(tc, n);
             }
         }
     };
-    fetch(a);
-    for (int64_t t = a; t < b; ++t) {
-        const float uv = un, zv = zn;
-        float dt = dn1 + bias;
-        if (s.softplus) {
-            const float e = softplus_exp(dt);
-            dt = softplus_end(dt, e, rcpf(e + 2.f));
-        }
-        const float du = dt * uv;
-        float4 bv[NV], cv[NV];
-#pragma unroll
-        for (int v = 0; v < NV; ++v) bv[v] = bn[v], cv[v] = cn[v];
-        const int ws = io.write_slots ? io.write_slots[t] : -1;
-        if (t + 1 < b) fetch(t + 1);
-        float acc[CPG];
-#pragma unroll
-        for (int k = 0; k < CPG; ++k) {
-            const float dk = __shfl_sync(0xffffffffu, dt, gr * QL + k), uk = __shfl_sync(0xffffffffu, du, gr * QL + k);
-            acc[k] = 0.f;
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                float4 &x = h[k][v];
-                x.x = fmaf(ex2f(dk * A[k][v].x), x.x, uk * bv[v].x);
-                x.y = fmaf(ex2f(dk * A[k][v].y), x.y, uk * bv[v].y);
-                x.z = fmaf(ex2f(dk * A[k][v].z), x.z, uk * bv[v].z);
-                x.w = fmaf(ex2f(dk * A[k][v].w), x.w, uk * bv[v].w);
-                acc[k] = fmaf(x.x, cv[v].x, acc[k]);
-                acc[k] = fmaf(x.y, cv[v].y, acc[k]);
-                acc[k] = fmaf(x.z, cv[v].z, acc[k]);
-                acc[k] = fmaf(x.w, cv[v].w, acc[k]);
-            }
-        }
-        if (ws >= s.num_slots) {
-            if (first) atomicOr(io.device_err, SSD_DEVERR_FINAL_SLOT);
-        } else if (ws >= 0) {
-#pragma unroll
-            for (int k = 0; k < CPG; ++k) {
-                const int ch = gr + GR * k;
-                float *dst = io.state_pool + (size_t)ws * dn + (size_t)(d0 + ch) * s.N;
-#pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    const int n0 = 4 * (l + QL * v), n = ch < width ? min(4, s.N - n0) : 0;
-                    const float4 x = h[k][v];
-                    if (p.vec) {
-                        if (n > 0) *reinterpret_cast<float4 *>(dst + n0) = x;
-                    } else {
-                        if (n > 0) dst[n0] = x.x;
-                        if (n > 1) dst[n0 + 1] = x.y;
-                        if (n > 2) dst[n0 + 2] = x.z;
-                        if (n > 3) dst[n0 + 3] = x.w;
-                    }
-                }
-            }
-        }
-        // sums over the QL lanes of a channel; lane k < CPG is left with channel k's
+    bool fetched = false;
+    for (int q = 0; q < count; ++q) {
+        stage(q + kRing - 1);
+        cp_wait<kRing - 1>();  // this lane's copies for request q have landed
+        const int a = __shfl_sync(0xffffffffu, ma, q), b = __shfl_sync(0xffffffffu, mb, q);
+        const int qn = min(q + 1, 31), an = __shfl_sync(0xffffffffu, ma, qn), bn = __shfl_sync(0xffffffffu, mb, qn);
+        if (a == b) continue;
+        if (!fetched) fetch(a);
+        float4 h[CPG][NV];
 #pragma unroll
         for (int k = 0; k < CPG; ++k)
 #pragma unroll
-            for (int o = QL / 2; o >= CPG; o >>= 1) acc[k] += __shfl_xor_sync(0xffffffffu, acc[k], o);
+            for (int v = 0; v < NV; ++v) h[k][v] = ring[q % kRing][k][v][tid];
+        for (int t = a; t < b; ++t) {
+            const auto now = in;
+            fetched = t + 1 < b || (q + 1 < count && an < bn);
+            if (fetched) fetch(t + 1 < b ? t + 1 : an);
+            float dt = now.dt + bias;
+            if (s.softplus) {
+                const float e = softplus_exp(dt);
+                dt = softplus_end(dt, e, rcpf(e + 2.f));
+            }
+            const float du = dt * now.u;
+            float acc[CPG];
 #pragma unroll
-        for (int o = CPG / 2; o >= 1; o >>= 1) {
-            const bool up = (l & o) != 0;
+            for (int k = 0; k < CPG; ++k) {
+                const float dk = __shfl_sync(0xffffffffu, dt, gr * QL + k);
+                const float uk = __shfl_sync(0xffffffffu, du, gr * QL + k);
+                acc[k] = 0.f;
 #pragma unroll
-            for (int k = 0; k < o; ++k) {
-                const float lo = acc[k], hi = acc[k + o];
-                acc[k] = (up ? hi : lo) + __shfl_xor_sync(0xffffffffu, up ? lo : hi, o);
+                for (int v = 0; v < NV; ++v) {
+                    float4 &x = h[k][v];
+                    x.x = fmaf(ex2f(dk * A[k][v].x), x.x, uk * now.b[v].x);
+                    x.y = fmaf(ex2f(dk * A[k][v].y), x.y, uk * now.b[v].y);
+                    x.z = fmaf(ex2f(dk * A[k][v].z), x.z, uk * now.b[v].z);
+                    x.w = fmaf(ex2f(dk * A[k][v].w), x.w, uk * now.b[v].w);
+                    acc[k] = fmaf(x.x, now.c[v].x, acc[k]);
+                    acc[k] = fmaf(x.y, now.c[v].y, acc[k]);
+                    acc[k] = fmaf(x.z, now.c[v].z, acc[k]);
+                    acc[k] = fmaf(x.w, now.c[v].w, acc[k]);
+                }
+            }
+            if (now.ws >= s.num_slots) {
+                if (tile == 0 && lane == 0) atomicOr(io.device_err, SSD_DEVERR_FINAL_SLOT);
+            } else if (now.ws >= 0) {
+                float *base = io.state_pool + (size_t)now.ws * dn;
+#pragma unroll
+                for (int k = 0; k < CPG; ++k)
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) {
+                        int n;
+                        float *dst = base + quad(k, v, n);
+                        const float4 x = h[k][v];
+                        if (p.vec) {
+                            if (n > 0) *reinterpret_cast<float4 *>(dst) = x;
+                        } else {
+                            if (n > 0) dst[0] = x.x;
+                            if (n > 1) dst[1] = x.y;
+                            if (n > 2) dst[2] = x.z;
+                            if (n > 3) dst[3] = x.w;
+                        }
+                    }
+            }
+            // sums over the QL lanes of a channel; lane k < CPG is left with channel k's
+#pragma unroll
+            for (int k = 0; k < CPG; ++k)
+#pragma unroll
+                for (int o = QL / 2; o >= CPG; o >>= 1) acc[k] += __shfl_xor_sync(0xffffffffu, acc[k], o);
+#pragma unroll
+            for (int o = CPG / 2; o >= 1; o >>= 1) {
+                const bool up = (l & o) != 0;
+#pragma unroll
+                for (int k = 0; k < o; ++k) {
+                    const float lo = acc[k], hi = acc[k + o];
+                    acc[k] = (up ? hi : lo) + __shfl_xor_sync(0xffffffffu, up ? lo : hi, o);
+                }
+            }
+            if (mine) {
+                float v = fmaf(skip, now.u, acc[0]);
+                if (z) v *= silu_sfu(now.z);
+                y[t * s.ys] = from_f32<T>(v);
             }
         }
-        if (mine) {
-            float v = fmaf(skip, uv, acc[0]);
-            if (z) v *= silu_sfu(zv);
-            y[t * s.ys] = from_f32<T>(v);
-        }
     }
+    cp_wait<0>();
 }
 
 template <typename T, int QL, int NV>
-cudaError_t launch_step_k(const SelStepParams &p, cudaStream_t stream) {
+cudaError_t launch_step_k(SelStepParams &p, cudaStream_t stream) {
     constexpr int CW = 32 / QL * (QL < 4 ? QL : 4), kWarps = kStepThreads / 32;
-    const int64_t items = (int64_t)((p.s.D / p.s.G + CW - 1) / CW) * p.s.G * p.s.R;
+    const int64_t tiles = (int64_t)((p.s.D / p.s.G + CW - 1) / CW) * p.s.G;
+    // requests a warp: as many as leave one wave of resident warps, so that none waits for a second
+    static int64_t cached[kResidentDevices] = {};
+    int64_t resident = 0;
+    const cudaError_t e = resident_ctas_at(cached, selective_step_kernel<T, QL, NV>, kStepThreads, 0, resident);
+    if (e != cudaSuccess) return e;
+    const int64_t wave = resident * kWarps;
+    p.rb = (int)std::min<int64_t>(kMaxRb, std::max<int64_t>(1, (tiles * p.s.R + wave - 1) / wave));
+    const int64_t items = tiles * ((p.s.R + p.rb - 1) / p.rb);
     if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     return launch_after_prev(selective_step_kernel<T, QL, NV>, dim3((unsigned)((items + kWarps - 1) / kWarps)),
                              dim3(kStepThreads), 0, stream, p);
@@ -211,7 +277,7 @@ cudaError_t launch_step_k(const SelStepParams &p, cudaStream_t stream) {
 
 // Lanes a channel: enough for its states at four a lane.
 template <typename T>
-cudaError_t launch_step(const SelStepParams &p, cudaStream_t stream) {
+cudaError_t launch_step(SelStepParams &p, cudaStream_t stream) {
     if (p.s.N <= 4) return launch_step_k<T, 1, 1>(p, stream);
     if (p.s.N <= 8) return launch_step_k<T, 2, 1>(p, stream);
     if (p.s.N <= 16) return launch_step_k<T, 4, 1>(p, stream);

@@ -25,7 +25,7 @@ namespace cg = cooperative_groups;
 namespace ssd {
 namespace {
 
-constexpr int kVerThreads = 512;
+constexpr int kVerThreads = 256;
 constexpr int kChunk = 1024;     // vocabulary entries of a warp's chunk
 constexpr int kMaxCluster = 8;   // the portable limit
 
@@ -115,8 +115,9 @@ __device__ __forceinline__ void load_weights(const Row<T> &row, int v, int V, fl
 template <typename T, int kVec>
 __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_constant__ VerifyParams p) {
     constexpr int kWarps = kVerThreads / 32, kLoads = kChunk / (32 * kVec);
+    constexpr int kBatch = kVec == 1 ? 16 : 4;  // loads of a row in flight a lane
     extern __shared__ unsigned long long chunk_sum[];  // of this CTA's chunks
-    __shared__ unsigned long long s_total;
+    __shared__ unsigned long long s_total, s_weight[kChunk + kChunk / 32];
     __shared__ int s_n;
     pdl_wait();
     cg::cluster_group cluster = cg::this_cluster();
@@ -128,6 +129,7 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
         if (rank == 0 && tid == 0) atomicOr(io.device_err, SSD_DEVERR_CU_SEQLENS);
         return;
     }
+    const float sample = io.sample_u ? io.sample_u[i] : 0.f;  // fetched early
     if (a == b) {
         if (rank == 0 && tid == 0) io.accepted[i] = -1;
         return;
@@ -175,12 +177,40 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
         for (int c = c0 + warp; c < c1; c += kWarps) {
             Digits d;
             const int v0 = c * kChunk + lane * kVec;
-#pragma unroll 8
-            for (int e = 0; e < kLoads; ++e) {
-                float w[kVec];
-                load_weights<T, kVec>(row, v0 + e * 32 * kVec, p.V, w);
+            const bool plain = (c + 1) * kChunk <= p.V && (unsigned)(row.drafted - c * kChunk) >= (unsigned)kChunk;
+            if (plain && row.q) {  // whole chunks: kBatch loads of each row in flight a lane
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) d.add(w[j]);
+                for (int e0 = 0; e0 < kLoads; e0 += kBatch) {
+                    float w[kBatch][kVec], q[kBatch][kVec];
+#pragma unroll
+                    for (int e = 0; e < kBatch; ++e) {
+                        load_probs<T, kVec>(row.p + v0 + (e0 + e) * 32 * kVec, w[e]);
+                        load_probs<T, kVec>(row.q + v0 + (e0 + e) * 32 * kVec, q[e]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < kBatch; ++e)
+#pragma unroll
+                        for (int j = 0; j < kVec; ++j) d.add(w[e][j] - q[e][j]);
+                }
+            } else if (plain) {
+#pragma unroll
+                for (int e0 = 0; e0 < kLoads; e0 += kBatch) {
+                    float w[kBatch][kVec];
+#pragma unroll
+                    for (int e = 0; e < kBatch; ++e) load_probs<T, kVec>(row.p + v0 + (e0 + e) * 32 * kVec, w[e]);
+#pragma unroll
+                    for (int e = 0; e < kBatch; ++e)
+#pragma unroll
+                        for (int j = 0; j < kVec; ++j) d.add(w[e][j]);
+                }
+            } else {
+                float w[kLoads][kVec];
+#pragma unroll
+                for (int e = 0; e < kLoads; ++e) load_weights<T, kVec>(row, v0 + e * 32 * kVec, p.V, w[e]);
+#pragma unroll
+                for (int e = 0; e < kLoads; ++e)
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j) d.add(w[e][j]);
             }
             const uint64_t sum = warp_sum(d.total(kLoads * kVec));
             if (lane == 0) chunk_sum[c - c0] = sum;
@@ -212,7 +242,7 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
         }
     }
     if (warp != 0 || total == 0) return;
-    const double f = (double)io.sample_u[i] * (double)total;
+    const double f = (double)sample * (double)total;
     unsigned long long mark = f >= 1.0 ? (unsigned long long)f : 0ull;  // 0 for a NaN too
     mark = min(mark, total - 1);
     if (mark < before) return;
@@ -240,44 +270,45 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
         }
     }
     if (hit < 0) return;  // a later CTA's
-#pragma unroll 1
-    for (int e = 0; e < kLoads; ++e) {
-        const int v0 = (c0 + hit) * kChunk + (e * 32 + lane) * kVec;
-        float w[kVec];
-        load_weights<T, kVec>(row, v0, p.V, w);
-        uint64_t each[kVec], sum = 0;
+    // The chunk's weights in the order of the vocabulary, 32 in a row a lane; a pad of one keeps the rows off each
+    // other's banks.
+    const int v0 = (c0 + hit) * kChunk;
+    float w[kLoads][kVec];
+#pragma unroll
+    for (int e = 0; e < kLoads; ++e) load_weights<T, kVec>(row, v0 + (e * 32 + lane) * kVec, p.V, w[e]);
+#pragma unroll
+    for (int e = 0; e < kLoads; ++e)
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
             Digits d;
-            d.add(w[j]);
-            sum += each[j] = d.total(1);
+            d.add(w[e][j]);
+            const int v = (e * 32 + lane) * kVec + j;
+            s_weight[v + v / 32] = d.total(1);
         }
-        const unsigned long long run = scan(sum);
-        const unsigned over = __ballot_sync(0xffffffffu, run > mark);
-        if (over) {
-            if (lane == __ffs(over) - 1) {
-                unsigned long long c = run - sum;
-                int v = v0;
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) {
-                    c += each[j];
-                    v += c <= mark;
-                }
-                io.out_tokens[r] = v;
-            }
-            return;
+    __syncwarp();
+    unsigned long long sum = 0;
+#pragma unroll 8
+    for (int j = 0; j < 32; ++j) sum += s_weight[lane * 33 + j];
+    const unsigned long long run = scan(sum);
+    if (lane == __ffs(__ballot_sync(0xffffffffu, run > mark)) - 1) {
+        unsigned long long c = run - sum;
+        int v = 0;
+#pragma unroll 8
+        for (int j = 0; j < 32; ++j) {  // entries whose running sum is not over the mark
+            c += s_weight[lane * 33 + j];
+            v += c <= mark;
         }
-        mark -= __shfl_sync(0xffffffffu, run, 31);
+        io.out_tokens[r] = v0 + lane * 32 + v;
     }
 }
 
 template <typename T, int kVec>
 cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream) {
     const int chunks = (p.V + kChunk - 1) / kChunk;
-    // CTAs a window: enough for two on every SM, but at least a chunk for each of a CTA's warps, so that few
+    // CTAs a window: enough for four on every SM, but at least a chunk for each of a CTA's warps, so that few
     // windows spread over the GPU and many do not pay for a cluster's barriers.
     int S = 1;
-    while (S < kMaxCluster && (int64_t)p.R * S < 2 * 152 && chunks >= 2 * S * (kVerThreads / 32)) S *= 2;
+    while (S < kMaxCluster && (int64_t)p.R * S < 4 * 152 && chunks >= 2 * S * (kVerThreads / 32)) S *= 2;
     const size_t smem = (size_t)((chunks + S - 1) / S + 1) * sizeof(unsigned long long);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
