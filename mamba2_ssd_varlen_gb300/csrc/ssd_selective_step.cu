@@ -23,7 +23,7 @@ namespace ssd {
 namespace {
 
 #ifndef STEP_MIN
-#define STEP_MIN 5
+#define STEP_MIN 4
 #endif
 #ifndef STEP_RING
 #define STEP_RING 3
@@ -55,7 +55,8 @@ __device__ __forceinline__ float4 some(const T *p, int n) {
 }
 
 // QL lanes a channel with 4 NV states each (quad v of a lane: states 4 (l + QL v) ..), CPG channels a lane group.
-template <typename T, int QL, int NV>
+// kExact: N = 4 QL NV, whole tiles of channels, everything on its boundary: no access is guarded, offsets are constants.
+template <typename T, int QL, int NV, bool kExact>
 __global__ void __launch_bounds__(kStepThreads, QL == 32 && NV == 2 ? 2 : STEP_MIN)
     selective_step_kernel(const __grid_constant__ SelStepParams p) {
     constexpr int GR = 32 / QL;               // lane groups of a warp
@@ -92,14 +93,15 @@ __global__ void __launch_bounds__(kStepThreads, QL == 32 && NV == 2 ? 2 : STEP_M
         }
     }
     // channel k of the group: gr + GR k, so that a warp's access covers neighbouring channels
-    auto quad = [&](int k, int v, int &n) {  // first state of quad (k, v), and how many of it there are
-        const int ch = gr + GR * k, n0 = 4 * (l + QL * v);
-        n = ch < width ? min(4, s.N - n0) : 0;
-        return (size_t)(d0 + ch) * s.N + n0;
+    const size_t at0 = (size_t)(d0 + gr) * s.N + 4 * l;  // the lane's first state
+    auto quad = [&](int k, int v, int &n) {  // quad (k, v) from there on, and how many of it there are
+        const int n0 = 4 * (l + QL * v);
+        n = kExact ? 4 : gr + GR * k < width ? min(4, s.N - n0) : 0;
+        return kExact ? (size_t)(GR * k * 4 * QL * NV + 4 * QL * v) : (size_t)GR * k * s.N + 4 * QL * v;
     };
     auto stage = [&](int q) {  // the states of request i0 + q, on their way
         const int slot = q < count ? __shfl_sync(0xffffffffu, ms, q) : -1;
-        const float *src = io.state_pool + (size_t)max(slot, 0) * dn;
+        const float *src = io.state_pool + (size_t)max(slot, 0) * dn + at0;
 #pragma unroll
         for (int k = 0; k < CPG; ++k)
 #pragma unroll
@@ -109,7 +111,7 @@ __global__ void __launch_bounds__(kStepThreads, QL == 32 && NV == 2 ? 2 : STEP_M
                 const size_t at = quad(k, v, n);
                 if (slot < 0 || n <= 0) {
                     *dst = make_float4(0.f, 0.f, 0.f, 0.f);
-                } else if (p.vec) {
+                } else if (kExact || p.vec) {
                     cp16(dst, src + at);
                 } else {
 #pragma unroll
@@ -133,44 +135,54 @@ __global__ void __launch_bounds__(kStepThreads, QL == 32 && NV == 2 ? 2 : STEP_M
             int n;
             const size_t at = quad(k, v, n);
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (n > 0) x = p.vec ? four(io.A + at) : some(io.A + at, n);
+            if (n > 0) x = kExact || p.vec ? four(io.A + at0 + at) : some(io.A + at0 + at, n);
             A[k][v] = make_float4(x.x * kLog2e, x.y * kLog2e, x.z * kLog2e, x.w * kLog2e);
         }
     // the lane's own channel (lanes past CPG have none)
     const int own = gr + GR * l, d = d0 + own;
     const bool mine = l < CPG && own < width;
     const float bias = mine && io.delta_bias ? io.delta_bias[d] : 0.f, skip = mine && io.D ? io.D[d] : 0.f;
-    const T *u = static_cast<const T *>(io.u) + d, *dl = static_cast<const T *>(io.delta) + d;
-    const T *z = io.z ? static_cast<const T *>(io.z) + d : nullptr;
-    const T *B = static_cast<const T *>(io.B) + (size_t)g * s.N, *C = static_cast<const T *>(io.C) + (size_t)g * s.N;
-    T *y = static_cast<T *>(io.y) + d;
-
+    // The windows of neighbouring requests follow one another, so rows are walked by adding their strides.
+    const T *pu, *pd, *pz, *pb, *pc;
+    const int32_t *pw;
+    auto seek = [&](int64_t t) {  // the row that the next fetch takes
+        pu = static_cast<const T *>(io.u) + t * s.us + d;
+        pd = static_cast<const T *>(io.delta) + t * s.ds + d;
+        pz = static_cast<const T *>(io.z) + t * s.zs + d;
+        pb = static_cast<const T *>(io.B) + t * s.bs + (size_t)g * s.N + 4 * l;
+        pc = static_cast<const T *>(io.C) + t * s.cs + (size_t)g * s.N + 4 * l;
+        pw = io.write_slots + t;
+    };
     // a token's inputs, fetched while the one before it is computed
     struct {
-        float u, dt, z;
+        T u, dt, z;
         int ws;
         float4 b[NV], c[NV];
-    } in = {};
-    auto fetch = [&](int64_t t) {
+    } in;
+    in.u = in.dt = in.z = from_f32<T>(0.f);
+    const bool gated = io.z != nullptr, keeps = io.write_slots != nullptr;
+    auto fetch = [&]() {
         if (mine) {
-            in.u = to_f32(u[t * s.us]);
-            in.dt = to_f32(dl[t * s.ds]);
-            if (z) in.z = to_f32(z[t * s.zs]);
+            in.u = *pu;
+            in.dt = *pd;
+            if (gated) in.z = *pz;
         }
-        in.ws = io.write_slots ? io.write_slots[t] : -1;
+        in.ws = keeps ? *pw : -1;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int n0 = 4 * (l + QL * v), n = min(4, s.N - n0);
-            const T *tb = B + t * s.bs + n0, *tc = C + t * s.cs + n0;
-            if (p.bc_vec && n > 0) {
-                in.b[v] = four(tb);
-                in.c[v] = four(tc);
+            const int n = kExact ? 4 : min(4, s.N - 4 * (l + QL * v));
+            if (kExact || (p.bc_vec && n > 0)) {
+                in.b[v] = four(pb + 4 * QL * v);
+                in.c[v] = four(pc + 4 * QL * v);
             } else {
-                in.b[v] = some(tb, n);
-                in.c[v] = some(tc, n);
+                in.b[v] = some(pb + 4 * QL * v, n);
+                in.c[v] = some(pc + 4 * QL * v, n);
             }
         }
+        pu += s.us, pd += s.ds, pz += s.zs, pb += s.bs, pc += s.cs, ++pw;
     };
+    T *py = nullptr;
+    int next = -1;  // the token that the fetch pointers are at, whose inputs are not fetched
     bool fetched = false;
     for (int q = 0; q < count; ++q) {
         stage(q + kRing - 1);
@@ -178,7 +190,11 @@ __global__ void __launch_bounds__(kStepThreads, QL == 32 && NV == 2 ? 2 : STEP_M
         const int a = __shfl_sync(0xffffffffu, ma, q), b = __shfl_sync(0xffffffffu, mb, q);
         const int qn = min(q + 1, 31), an = __shfl_sync(0xffffffffu, ma, qn), bn = __shfl_sync(0xffffffffu, mb, qn);
         if (a == b) continue;
-        if (!fetched) fetch(a);
+        if (!fetched) {
+            if (next != a) seek(a);
+            fetch();
+        }
+        py = static_cast<T *>(io.y) + a * s.ys + d;
         float4 h[CPG][NV];
 #pragma unroll
         for (int k = 0; k < CPG; ++k)
@@ -186,14 +202,16 @@ __global__ void __launch_bounds__(kStepThreads, QL == 32 && NV == 2 ? 2 : STEP_M
             for (int v = 0; v < NV; ++v) h[k][v] = ring[q % kRing][k][v][tid];
         for (int t = a; t < b; ++t) {
             const auto now = in;
-            fetched = t + 1 < b || (q + 1 < count && an < bn);
-            if (fetched) fetch(t + 1 < b ? t + 1 : an);
-            float dt = now.dt + bias;
+            const float uv = to_f32(now.u);
+            next = t + 1;
+            fetched = t + 1 < b || (q + 1 < count && an == b && an < bn);
+            if (fetched) fetch();
+            float dt = to_f32(now.dt) + bias;
             if (s.softplus) {
                 const float e = softplus_exp(dt);
                 dt = softplus_end(dt, e, rcpf(e + 2.f));
             }
-            const float du = dt * now.u;
+            const float du = dt * uv;
             float acc[CPG];
 #pragma unroll
             for (int k = 0; k < CPG; ++k) {
@@ -216,7 +234,7 @@ __global__ void __launch_bounds__(kStepThreads, QL == 32 && NV == 2 ? 2 : STEP_M
             if (now.ws >= s.num_slots) {
                 if (tile == 0 && lane == 0) atomicOr(io.device_err, SSD_DEVERR_FINAL_SLOT);
             } else if (now.ws >= 0) {
-                float *base = io.state_pool + (size_t)now.ws * dn;
+                float *base = io.state_pool + (size_t)now.ws * dn + at0;
 #pragma unroll
                 for (int k = 0; k < CPG; ++k)
 #pragma unroll
@@ -224,7 +242,7 @@ __global__ void __launch_bounds__(kStepThreads, QL == 32 && NV == 2 ? 2 : STEP_M
                         int n;
                         float *dst = base + quad(k, v, n);
                         const float4 x = h[k][v];
-                        if (p.vec) {
+                        if (kExact || p.vec) {
                             if (n > 0) *reinterpret_cast<float4 *>(dst) = x;
                         } else {
                             if (n > 0) dst[0] = x.x;
@@ -249,30 +267,37 @@ __global__ void __launch_bounds__(kStepThreads, QL == 32 && NV == 2 ? 2 : STEP_M
                 }
             }
             if (mine) {
-                float v = fmaf(skip, now.u, acc[0]);
-                if (z) v *= silu_sfu(now.z);
-                y[t * s.ys] = from_f32<T>(v);
+                float v = fmaf(skip, uv, acc[0]);
+                if (gated) v *= silu_sfu(to_f32(now.z));
+                *py = from_f32<T>(v);
             }
+            py += s.ys;
         }
     }
     cp_wait<0>();
 }
 
-template <typename T, int QL, int NV>
-cudaError_t launch_step_k(SelStepParams &p, cudaStream_t stream) {
+template <typename T, int QL, int NV, bool kExact>
+cudaError_t launch_step_e(SelStepParams &p, cudaStream_t stream) {
     constexpr int CW = 32 / QL * (QL < 4 ? QL : 4), kWarps = kStepThreads / 32;
-    const int64_t tiles = (int64_t)((p.s.D / p.s.G + CW - 1) / CW) * p.s.G;
-    // requests a warp: as many as leave one wave of resident warps, so that none waits for a second
+    constexpr auto kernel = selective_step_kernel<T, QL, NV, kExact>;
     static int64_t cached[kResidentDevices] = {};
     int64_t resident = 0;
-    const cudaError_t e = resident_ctas_at(cached, selective_step_kernel<T, QL, NV>, kStepThreads, 0, resident);
+    const cudaError_t e = resident_ctas_at(cached, kernel, kStepThreads, 0, resident);
     if (e != cudaSuccess) return e;
-    const int64_t wave = resident * kWarps;
+    // requests a warp: as many as leave one wave of resident warps, so that none waits for a second
+    const int64_t tiles = (int64_t)((p.s.D / p.s.G + CW - 1) / CW) * p.s.G, wave = resident * kWarps;
     p.rb = (int)std::min<int64_t>(kMaxRb, std::max<int64_t>(1, (tiles * p.s.R + wave - 1) / wave));
     const int64_t items = tiles * ((p.s.R + p.rb - 1) / p.rb);
     if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    return launch_after_prev(selective_step_kernel<T, QL, NV>, dim3((unsigned)((items + kWarps - 1) / kWarps)),
-                             dim3(kStepThreads), 0, stream, p);
+    return launch_after_prev(kernel, dim3((unsigned)((items + kWarps - 1) / kWarps)), dim3(kStepThreads), 0, stream, p);
+}
+
+template <typename T, int QL, int NV>
+cudaError_t launch_step_k(SelStepParams &p, cudaStream_t stream) {
+    constexpr int CW = 32 / QL * (QL < 4 ? QL : 4);
+    const bool exact = p.s.N == 4 * QL * NV && p.s.D / p.s.G % CW == 0 && p.vec && p.bc_vec;
+    return exact ? launch_step_e<T, QL, NV, true>(p, stream) : launch_step_e<T, QL, NV, false>(p, stream);
 }
 
 // Lanes a channel: enough for its states at four a lane.
