@@ -6,6 +6,34 @@
 
 namespace ssd {
 
+// Packed fp32 pairs (one 64-bit register pair): two products or sums an issue slot.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pk(float lo, float hi) {
+    f2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ float2 upk(f2 d) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 __device__ __forceinline__ float ex2f(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -46,6 +74,27 @@ __device__ __forceinline__ float softplus_end(float v, float e, float r) {
     p = fmaf(p, q, 2.f / 3.f);
     p = fmaf(p * q, s, s + s);
     return fmaxf(v, 0.f) + p;
+}
+
+// The same for a packed pair.
+__device__ __forceinline__ f2 softplus_exp(f2 v) {
+    const float2 w = upk(v);
+    const f2 t = pk(max_nan(-fabsf(w.x), -200.f), max_nan(-fabsf(w.y), -200.f));
+    const f2 x = mul2(t, pk(kLog2e, kLog2e));
+    const float2 y = upk(x);
+    const f2 e = pk(ex2f(y.x), ex2f(y.y));
+    return fma2(e, fma2(x, pk(-kLn2, -kLn2), t), e);
+}
+__device__ __forceinline__ f2 softplus_end(f2 v, f2 e, f2 r) {
+    const f2 s = mul2(e, r), q = mul2(s, s);
+    f2 p = fma2(q, pk(2.f / 13.f, 2.f / 13.f), pk(2.f / 11.f, 2.f / 11.f));
+    p = fma2(p, q, pk(2.f / 9.f, 2.f / 9.f));
+    p = fma2(p, q, pk(2.f / 7.f, 2.f / 7.f));
+    p = fma2(p, q, pk(2.f / 5.f, 2.f / 5.f));
+    p = fma2(p, q, pk(2.f / 3.f, 2.f / 3.f));
+    p = fma2(mul2(p, q), s, add2(s, s));
+    const float2 w = upk(v);
+    return add2(pk(fmaxf(w.x, 0.f), fmaxf(w.y, 0.f)), p);
 }
 
 // silu(z) = z / (1 + exp(-z)).

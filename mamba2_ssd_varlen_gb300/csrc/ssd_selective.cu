@@ -19,6 +19,8 @@
 //     for different tokens, and exchanged through shared memory.  They, and the sums over
 //     the L lanes, belong to the blocks of TB tokens after and before the one whose
 //     recurrence runs beside them, so that their latency hides behind it.
+#include <algorithm>
+
 #include "async_copy.cuh"
 #include "pdl.cuh"
 #include "selective.cuh"
@@ -30,8 +32,8 @@ namespace {
 constexpr int kTile = 16;  // tokens staged at a time
 constexpr int kCh = 32;    // channels of a CTA
 constexpr int kPairs = kCh / 2;
-#ifndef SEL_MIN
-#define SEL_MIN 1
+#ifndef SEL_REGS
+#define SEL_REGS 160
 #endif
 
 struct SelParams {
@@ -42,6 +44,9 @@ struct SelParams {
     int32_t vec;     // u, delta, z: every tile row of a CTA starts on a 16-byte boundary
     int32_t bc_vec;  // B, C: every four states of a row start on a boundary of four elements
     int32_t y_pair;  // y: every pair of channels starts on a boundary of two elements
+    int32_t seg;     // tiles of a segment where requests are split over the time; 0: not split
+    float *seg_state;  // (segment places, D, N): the state after a segment that entered it with zeros
+    float *seg_steps;  // (segment places, D): the sum of its steps
 };
 
 template <typename T>
@@ -103,6 +108,9 @@ struct Cfg {
     static constexpr int WARPS = (THREADS + 31) / 32;
     static constexpr int QUADS = kTile * NP / 4;   // (row, four states) of a tile of B or C
     static constexpr int IT = (QUADS + THREADS - 1) / THREADS;
+    // registers a thread: what the states, the decay rates and a block's work need without spilling
+    static constexpr int REGS = NS <= 4 ? SEL_REGS : NS <= 8 ? 224 : 255;
+    static constexpr int MIN = 65536 / (THREADS * REGS) > 1 ? 65536 / (THREADS * REGS) : 1;
     static_assert(NS >= 1 && kTile % TB == 0 && L <= 16, "whole blocks, a pair inside a warp");
     struct Smem {
         T raw[3][3][kTile][kCh];        // u, delta, z of the tile at hand, the next and the one in flight
@@ -118,9 +126,27 @@ __device__ __forceinline__ void cta_sync() {
     else __syncthreads();
 }
 
+// Requests split over the time: request i's segments sit at places seg_place(i), seg_place(i) + 1, ...; it has at most
+// (length + 15) / (16 seg) + 1 of them, so that the next request's first place is past its last, and a place's request is
+// found by a binary search in cu_seqlens alone.
+__device__ __forceinline__ int seg_place(const SelParams &p, int i) {
+    return (int)(((int64_t)p.cu[i] + (int64_t)kTile * i) / ((int64_t)kTile * p.seg)) + i;
+}
+__device__ __forceinline__ int seg_request(const SelParams &p, int place) {
+    int lo = 0, hi = p.s.R;  // seg_place(lo) <= place, the answer in [lo, hi)
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (seg_place(p, mid) <= place) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+inline int64_t seg_places(int64_t T, int64_t R, int64_t seg) { return (T + kTile * R) / (kTile * seg) + R; }
+
 // kCommon: softplus, a gate, and pairs of y on their boundaries (what a layer has); else these are looked up.
-template <typename T, int NP, int L, bool kCommon>
-__global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __grid_constant__ SelParams p) {
+// kStates: only the states that segments leave behind, from zeros; no outputs.
+template <typename T, int NP, int L, bool kCommon, bool kStates>
+__global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kernel(const __grid_constant__ SelParams p) {
     using K = Cfg<T, NP, L>;
     constexpr int NS = K::NS, PW = K::PW, OWN = K::OWN, TB = K::TB, THREADS = K::THREADS, IT = K::IT;
     extern __shared__ __align__(16) uint8_t sel_smem[];
@@ -131,19 +157,29 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int l = lane / PW, pr = lane % PW;       // this lane's share of the states, its pair in the warp
     const int c = (warp * PW + pr) * 2;            // the pair's first channel in the tile
-    const int i = (int)(blockIdx.x / p.tiles), tile = (int)(blockIdx.x % p.tiles);
+    const int tile = (int)(blockIdx.x % p.tiles);
+    int i = (int)(blockIdx.x / p.tiles), place = i;
+    if (p.seg) {
+        i = seg_request(p, place);
+        if (blockIdx.x == 0) {  // the places of a wrong cu_seqlens may leave out requests: all are looked at here
+            for (int q = tid; q < s.R; q += THREADS)
+                if (p.cu[q + 1] < p.cu[q] || (q == 0 && p.cu[0] != 0) || (q == s.R - 1 && p.cu[s.R] != s.T))
+                    atomicOr(io.device_err, SSD_DEVERR_CU_SEQLENS);
+        }
+    }
     const int dg = s.D / s.G, per_group = p.tiles / s.G;
     const int g = tile / per_group, off = (tile % per_group) * kCh;
     const int width = min(kCh, dg - off);          // channels of this CTA
     const int d0 = g * dg + off, d = d0 + c;
     const bool mine[2] = {c < width, c + 1 < width};
-    const bool first = tile == 0 && tid == 0;
 
     const int64_t a = p.cu[i], b = p.cu[i + 1];
     if (b < a || a < 0 || b > s.T || (i == 0 && a != 0) || (i == s.R - 1 && b != s.T)) {
-        if (first) atomicOr(io.device_err, SSD_DEVERR_CU_SEQLENS);
+        if (tile == 0 && tid == 0) atomicOr(io.device_err, SSD_DEVERR_CU_SEQLENS);
         return;
     }
+    const int part = p.seg ? place - seg_place(p, i) : 0;  // the segment of the request
+    const bool first = tile == 0 && tid == 0;
     const int len = (int)(b - a);
     int done = 0;
     bool table = io.block_table != nullptr;
@@ -157,14 +193,17 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
     }
 
     const T *gu = static_cast<const T *>(io.u) + a * s.us + d0, *gd = static_cast<const T *>(io.delta) + a * s.ds + d0;
-    const T *gz = kCommon || io.z ? static_cast<const T *>(io.z) + a * s.zs + d0 : nullptr;
+    const T *gz = !kStates && (kCommon || io.z) ? static_cast<const T *>(io.z) + a * s.zs + d0 : nullptr;
     const T *gb = static_cast<const T *>(io.B) + a * s.bs + (size_t)g * s.N;
     const T *gc = static_cast<const T *>(io.C) + a * s.cs + (size_t)g * s.N;
     T *gy = static_cast<T *>(io.y) + a * s.ys + d;
 
     // Tiles end at absolute multiples of kTile where block states are kept, so that a boundary ends its tile.
     const int lead = table ? done % kTile : 0;
-    const int tiles = (lead + len + kTile - 1) / kTile;
+    const int all = (lead + len + kTile - 1) / kTile;     // tiles of the request
+    const int from = part * p.seg, tiles = p.seg ? min(all, from + p.seg) : all;  // of this segment: from .. tiles - 1
+    const bool ends = tiles == all;
+    if ((part > 0 && from >= all) || (kStates && ends)) return;  // no such segment; nobody needs its state
     auto tile_begin = [&](int k) { return k == 0 ? 0 : k * kTile - lead; };
     auto rows_of = [&](int k) { return min(len, (k + 1) * kTile - lead) - tile_begin(k); };
     auto stage = [&](int k) {  // asynchronous copies of u, delta and z of tile k
@@ -178,7 +217,7 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
                 const size_t t = t0 + r;
                 cp16(&sm.raw[st][0][r][col], gu + t * s.us + col);
                 cp16(&sm.raw[st][1][r][col], gd + t * s.ds + col);
-                if (kCommon || gz) cp16(&sm.raw[st][2][r][col], gz + t * s.zs + col);
+                if (!kStates && (kCommon || gz)) cp16(&sm.raw[st][2][r][col], gz + t * s.zs + col);
             }
         } else {
             for (int q = tid; q < n * kCh; q += THREADS) {
@@ -187,7 +226,7 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
                 const size_t t = t0 + r;
                 cp_elem(&sm.raw[st][0][r][col], gu + t * s.us + col);
                 cp_elem(&sm.raw[st][1][r][col], gd + t * s.ds + col);
-                if (kCommon || gz) cp_elem(&sm.raw[st][2][r][col], gz + t * s.zs + col);
+                if (!kStates && (kCommon || gz)) cp_elem(&sm.raw[st][2][r][col], gz + t * s.zs + col);
             }
         }
         cp_commit();
@@ -232,7 +271,7 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
     float2 h[NS], A[NS];
     {
         const float *src = nullptr;
-        if (io.init_slots) {
+        if (!kStates && io.init_slots) {
             const int slot = io.init_slots[i];
             if (slot >= s.num_slots) {
                 if (first) atomicOr(io.device_err, SSD_DEVERR_INIT_SLOT);
@@ -252,6 +291,18 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
             }
             h[k] = make_float2(hv[0], hv[1]);
             A[k] = make_float2(av[0], av[1]);
+        }
+    }
+    if (!kStates && part > 0) {  // through the request's segments before this one
+        for (int q = place - part; q < place; ++q) {
+            const float *st = p.seg_steps + (size_t)q * s.D + d, *sv = p.seg_state + (size_t)q * dn + row;
+            const float2 steps = make_float2(mine[0] ? st[0] : 0.f, mine[1] ? st[1] : 0.f);
+#pragma unroll
+            for (int k = 0; k < NS; ++k) {
+                const bool ok = n0 + k < s.N;
+                h[k].x = fmaf(ex2f(steps.x * A[k].x), h[k].x, ok && mine[0] ? sv[n0 + k] : 0.f);
+                h[k].y = fmaf(ex2f(steps.y * A[k].y), h[k].y, ok && mine[1] ? sv[s.N + n0 + k] : 0.f);
+            }
         }
     }
     auto two = [&](const float *v) { return make_float2(v && mine[0] ? v[d] : 0.f, v && mine[1] ? v[d + 1] : 0.f); };
@@ -274,7 +325,7 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
     struct Steps {
         float2 v[OWN], e[OWN], r[OWN], z[OWN], ze[OWN];
     };
-    const bool softplus = kCommon || s.softplus, gated = kCommon || gz != nullptr;
+    const bool softplus = kCommon || s.softplus, gated = !kStates && (kCommon || gz != nullptr);
     // Four stages, each taking up what the special-function unit gave the one before it.
     auto prepare = [&](int stage, Own &o, Steps &w, const T *r, int x) {
 #pragma unroll
@@ -286,15 +337,17 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
                 w.v[q].y += bias.y;
                 if (gated) w.z[q] = load_pair(r + (2 * kTile + q) * kCh);
             } else if (stage == 1) {
-                if (softplus) w.e[q] = make_float2(softplus_exp(w.v[q].x), softplus_exp(w.v[q].y));
-                if (gated) w.ze[q] = make_float2(ex2f(-kLog2e * w.z[q].x), ex2f(-kLog2e * w.z[q].y));
+                if (softplus) w.e[q] = upk(softplus_exp(pk(w.v[q].x, w.v[q].y)));
+                if (gated) {
+                    const float2 x = upk(mul2(pk(w.z[q].x, w.z[q].y), pk(-kLog2e, -kLog2e)));
+                    w.ze[q] = make_float2(ex2f(x.x), ex2f(x.y));
+                }
             } else if (stage == 2) {
                 if (softplus) w.r[q] = make_float2(rcpf(w.e[q].x + 2.f), rcpf(w.e[q].y + 2.f));
                 if (gated) o.gate[q] = make_float2(rcpf(1.f + w.ze[q].x), rcpf(1.f + w.ze[q].y));
             } else {
                 if (softplus)
-                    w.v[q] = make_float2(softplus_end(w.v[q].x, w.e[q].x, w.r[q].x),
-                                         softplus_end(w.v[q].y, w.e[q].y, w.r[q].y));
+                    w.v[q] = upk(softplus_end(pk(w.v[q].x, w.v[q].y), pk(w.e[q].x, w.e[q].y), pk(w.r[q].x, w.r[q].y)));
                 if (gated) {
                     o.gate[q].x *= w.z[q].x;
                     o.gate[q].y *= w.z[q].y;
@@ -311,13 +364,13 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
         for (int q = 0; q < OWN; ++q) {
             const int j = l * OWN + q;
             if (stage == 0) {
-                out[q] = make_float2(0.f, 0.f);
+                f2 v = 0;
 #pragma unroll
                 for (int e = 0; e < L; ++e) {  // lane l starts with its own column: no two lanes in one bank
-                    const float2 w = sm.yp[x][warp][j][lane ^ e * PW];
-                    out[q].x += w.x;
-                    out[q].y += w.y;
+                    const f2 w = *reinterpret_cast<const f2 *>(&sm.yp[x][warp][j][lane ^ e * PW]);
+                    v = e ? add2(v, w) : w;
                 }
+                out[q] = upk(v);
             } else {
                 float2 v = make_float2(fmaf(skip.x, o.uv[q].x, out[q].x), fmaf(skip.y, o.uv[q].y, out[q].y));
                 if (gated) {
@@ -336,31 +389,32 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
     };
 
     // Tile k is computed while tile k + 1 (landed) is prepared for and tile k + 2 is in flight.
-    if (tiles > 0 && len > 0) {
-        stage(0);
-        if (tiles > 1) stage(1);
-        fetch_bc(0);
-        widen_bc(0);
-        if (tiles > 1) cp_wait<1>();
+    float2 steps = make_float2(0.f, 0.f);  // their sum over the segment
+    if (tiles > from && len > 0) {
+        stage(from);
+        if (tiles > from + 1) stage(from + 1);
+        fetch_bc(from);
+        widen_bc(from);
+        if (tiles > from + 1) cp_wait<1>();
         else cp_wait<0>();
         cta_sync<THREADS>();
-        int buf = 0;                       // raw buffer of the tile at hand
+        int buf = from % 3;                // raw buffer of the tile at hand
         auto raw_row = [&](int which) { return &sm.raw[which][0][l * OWN][c]; };
         Own before = {}, now, next;        // the block computed last, the one at hand, the one prepared beside it
         {
             Steps w;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) prepare(e, now, w, raw_row(0), 0);
+            for (int e = 0; e < 4; ++e) prepare(e, now, w, raw_row(buf), 0);
         }
-        T *yp = gy + (int64_t)(l * OWN - TB) * s.ys;  // y of the lane's first token in the block before
+        T *yp = gy + ((int64_t)tile_begin(from) + l * OWN - TB) * s.ys;  // y of the lane's first token in the block before
         int before_valid = 0;                         // and how many of that block's tokens there are
         const int64_t y_step = (int64_t)TB * s.ys;
         // One block of tile k: the recurrence of its tokens, and between them, a stage at a time, the steps of the next
         // block (rows from r on) and the outputs of the one before.  x: the exchange buffer of this block.
         auto block = [&](const float2 *f, const T *r, int x, int valid, auto full) {
             Steps w;
-            float2 acc[TB], out[OWN];
-            finish(0, out, before, x ^ 1, yp, before_valid);
+            float2 acc[TB], out[OWN], sum = make_float2(0.f, 0.f);
+            if (!kStates) finish(0, out, before, x ^ 1, yp, before_valid);
             prepare(0, next, w, r, x ^ 1);
 #pragma unroll
             for (int j = 0; j < TB; ++j) {
@@ -380,21 +434,31 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
                     }
 #pragma unroll
                     for (int q = 0; q < NS; ++q) {
-                        h[q].x = fmaf(ex2f(dd.x * A[q].x), h[q].x, dd.z * bc[q].x);
-                        h[q].y = fmaf(ex2f(dd.y * A[q].y), h[q].y, dd.w * bc[q].x);
-                        acc[j].x = q == 0 ? h[q].x * bc[q].y : fmaf(h[q].x, bc[q].y, acc[j].x);
-                        acc[j].y = q == 0 ? h[q].y * bc[q].y : fmaf(h[q].y, bc[q].y, acc[j].y);
+                        const float2 x = upk(mul2(pk(dd.x, dd.y), pk(A[q].x, A[q].y)));
+                        h[q].x = fmaf(ex2f(x.x), h[q].x, dd.z * bc[q].x);
+                        h[q].y = fmaf(ex2f(x.y), h[q].y, dd.w * bc[q].x);
+                        if (!kStates) {
+                            acc[j].x = q == 0 ? h[q].x * bc[q].y : fmaf(h[q].x, bc[q].y, acc[j].x);
+                            acc[j].y = q == 0 ? h[q].y * bc[q].y : fmaf(h[q].y, bc[q].y, acc[j].y);
+                        }
                     }
+                    sum.x += dd.x;
+                    sum.y += dd.y;
                 }
-                if (j == 0) finish(1, out, before, x ^ 1, yp, before_valid);
+                if (!kStates && j == 0) finish(1, out, before, x ^ 1, yp, before_valid);
                 if (TB <= 4) {
                     if (j < 3) prepare(j + 1, next, w, r, x ^ 1);
                 } else if (j % (TB / 4) == 0 && j / (TB / 4) < 3) {
                     prepare(j / (TB / 4) + 1, next, w, r, x ^ 1);
                 }
             }
+            if (kStates) {
+                steps.x += sum.x;
+                steps.y += sum.y;
+            } else {
 #pragma unroll
-            for (int j = 0; j < TB; ++j) sm.yp[x][warp][j][lane] = acc[j];
+                for (int j = 0; j < TB; ++j) sm.yp[x][warp][j][lane] = acc[j];
+            }
             before = now;
             now = next;
             before_valid = valid;
@@ -402,7 +466,7 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
         };
         constexpr int NB = kTile / TB;     // blocks of a tile: an even number, so the exchange buffers alternate in step
         static_assert(NB % 2 == 0, "parity");
-        for (int k = 0; k < tiles; ++k) {
+        for (int k = from; k < tiles; ++k) {
             const int t0 = tile_begin(k), n = rows_of(k), buf1 = buf == 2 ? 0 : buf + 1;
             cp_wait<0>();
             cta_sync<THREADS>();  // tile k + 1 has landed, B and C of tile k are laid out, tile k - 1 is computed
@@ -423,15 +487,17 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
                     block(f + q * TB * NP, q + 1 < NB ? r0 + (q + 1) * TB * kCh : r1, q & 1, n - q * TB, Flag<false>{});
                     yp += y_step;
                 }
-                float2 out[OWN];
-                finish(0, out, before, 1, yp, before_valid);
-                finish(1, out, before, 1, yp, before_valid);
+                if (!kStates) {
+                    float2 out[OWN];
+                    finish(0, out, before, 1, yp, before_valid);
+                    finish(1, out, before, 1, yp, before_valid);
+                }
                 before_valid = 0;
                 yp -= skipped;    // the next tile's rows follow the last that is there
             }
             buf = buf1;
             if (k + 1 < tiles) widen_bc(k + 1);
-            if (table) {
+            if (!kStates && table) {
                 const int pos = done + t0 + n;
                 if (pos % s.block_size == 0) {
                     const int col = pos / s.block_size - 1;
@@ -448,10 +514,19 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
                 }
             }
         }
-        float2 out[OWN];
-        finish(0, out, before, 1, yp, before_valid);
-        finish(1, out, before, 1, yp, before_valid);
+        if (!kStates) {
+            float2 out[OWN];
+            finish(0, out, before, 1, yp, before_valid);
+            finish(1, out, before, 1, yp, before_valid);
+        }
     }
+    if (kStates) {
+        put(p.seg_state + (size_t)place * dn);
+        if (l == 0 && mine[0]) p.seg_steps[(size_t)place * s.D + d] = steps.x;
+        if (l == 0 && mine[1]) p.seg_steps[(size_t)place * s.D + d + 1] = steps.y;
+        return;
+    }
+    if (!ends) return;
     if (io.final_states) put(io.final_states + (size_t)i * dn);
     if (io.final_slots) {
         const int slot = io.final_slots[i];
@@ -463,20 +538,26 @@ __global__ void __launch_bounds__(kPairs * L, SEL_MIN) selective_kernel(const __
     }
 }
 
-template <typename T, int NP, int L, bool kCommon>
+template <typename T, int NP, int L, bool kCommon, bool kStates>
 cudaError_t launch_g(const SelParams &p, cudaStream_t stream) {
-    constexpr auto kernel = selective_kernel<T, NP, L, kCommon>;
+    constexpr auto kernel = selective_kernel<T, NP, L, kCommon, kStates>;
     constexpr size_t smem = sizeof(typename Cfg<T, NP, L>::Smem);
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    return launch_after_prev(kernel, dim3((unsigned)((int64_t)p.tiles * p.s.R)), dim3(kPairs * L), smem, stream, p);
+    const int64_t rows = p.seg ? seg_places(p.s.T, p.s.R, p.seg) : p.s.R;
+    return launch_after_prev(kernel, dim3((unsigned)(p.tiles * rows)), dim3(kPairs * L), smem, stream, p);
 }
 
 template <typename T, int NP, int L>
 cudaError_t launch_k(const SelParams &p, cudaStream_t stream) {
-    return p.s.softplus && p.io.z && p.y_pair ? launch_g<T, NP, L, true>(p, stream) : launch_g<T, NP, L, false>(p, stream);
+    if (p.seg) {
+        const cudaError_t e = launch_g<T, NP, L, false, true>(p, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return p.s.softplus && p.io.z && p.y_pair ? launch_g<T, NP, L, true, false>(p, stream)
+                                              : launch_g<T, NP, L, false, false>(p, stream);
 }
 
 #ifndef SEL_L16
@@ -494,14 +575,31 @@ cudaError_t launch(const SelParams &p, cudaStream_t stream) {
     return launch_k<T, 256, 8>(p, stream);
 }
 
+// Channel tiles of a request.
+int64_t channel_tiles(const ssd_selective_dims *d) {
+    const int dg = d->D / d->G;
+    return (int64_t)d->G * ((dg + kCh - 1) / kCh);
+}
+
+// Tiles of a segment, 0 where requests are not split.  With few CTAs the recurrence of a long request is latency; split
+// over the time its states are computed twice, but by as many CTAs as the GPU holds at once (six an SM).  Not for fewer
+// than three segments, which would not pay for the second pass.
+int segment_tiles(const ssd_selective_dims *d) {
+    const int64_t parts = 6 * 152 / (channel_tiles(d) * d->R), tiles = d->T / d->R / kTile;  // of a mean request
+    if (parts < 3 || tiles < 32) return 0;
+    return (int)std::max<int64_t>(8, (tiles + parts) / parts);
+}
+
 }  // namespace
 }  // namespace ssd
 
 using namespace ssd;
 
 extern "C" size_t ssd_varlen_selective_scan_workspace(const ssd_selective_dims *d) {
-    (void)d;
-    return 0;
+    SelShape s;
+    if (!d || sel_shape(d, false, &s) != SSD_OK) return 0;
+    const int seg = segment_tiles(d);
+    return seg ? (size_t)seg_places(d->T, d->R, seg) * d->D * (d->N + 1) * sizeof(float) : 0;
 }
 
 extern "C" int ssd_varlen_selective_scan(const ssd_selective_dims *d, const int32_t *cu_seqlens,
@@ -527,8 +625,14 @@ extern "C" int ssd_varlen_selective_scan(const ssd_selective_dims *d, const int3
     if (need && (!io->workspace || io->workspace_bytes < need || !sel_aligned(io->workspace, 16)))
         return SSD_ERR_WORKSPACE;
     const int dg = d->D / d->G;
-    const int64_t tiles = (int64_t)d->G * ((dg + kCh - 1) / kCh);
-    if (tiles * d->R > 0x7fffffffLL) return SSD_ERR_DIMS;
+    const int64_t tiles = channel_tiles(d);
+    p.seg = segment_tiles(d);
+    const int64_t rows_of_ctas = p.seg ? seg_places(d->T, d->R, p.seg) : d->R;
+    if (tiles * rows_of_ctas > 0x7fffffffLL) return SSD_ERR_DIMS;
+    if (p.seg) {
+        p.seg_state = static_cast<float *>(io->workspace);
+        p.seg_steps = p.seg_state + (size_t)rows_of_ctas * d->D * d->N;
+    }
     p.cu = cu_seqlens;
     p.io = *io;
     p.tiles = (int32_t)tiles;

@@ -87,35 +87,56 @@ struct Row {
     int drafted;     // the token that 1 is taken off, or -1
 };
 
-// kVec weights from entry v on, zeros past V.
+// The weights of chunk c, kVec neighbouring ones a load, lane by lane; zeros past V.  Every load is issued before a
+// value is used.
 template <typename T, int kVec>
-__device__ __forceinline__ void load_weights(const Row<T> &row, int v, int V, float (&w)[kVec]) {
-    if (v + kVec <= V) {
-        load_probs<T, kVec>(row.p + v, w);
-        if (row.q) {
-            float q[kVec];
-            load_probs<T, kVec>(row.q + v, q);
+__device__ __forceinline__ void load_chunk(const Row<T> &row, int c, int lane, int V,
+                                           float (&w)[kChunk / (32 * kVec)][kVec]) {
+    constexpr int kLoads = kChunk / (32 * kVec);
+    const int v0 = c * kChunk + lane * kVec;
+    float q[kLoads][kVec];
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) w[e] -= q[e];
-        }
-    } else {
+    for (int e = 0; e < kLoads; ++e) {
+        const int v = v0 + e * 32 * kVec;
+        if (v + kVec <= V) {
+            load_probs<T, kVec>(row.p + v, w[e]);
+        } else {
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            w[e] = v + e < V ? to_f32(row.p[v + e]) : 0.f;
-            if (row.q && v + e < V) w[e] -= to_f32(row.q[v + e]);
+            for (int j = 0; j < kVec; ++j) w[e][j] = v + j < V ? to_f32(row.p[v + j]) : 0.f;
         }
     }
-    if ((unsigned)(row.drafted - v) < (unsigned)kVec) {
+    if (row.q) {
 #pragma unroll
-        for (int e = 0; e < kVec; ++e)
-            if (v + e == row.drafted) w[e] -= 1.f;
+        for (int e = 0; e < kLoads; ++e) {
+            const int v = v0 + e * 32 * kVec;
+            if (v + kVec <= V) {
+                load_probs<T, kVec>(row.q + v, q[e]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) q[e][j] = v + j < V ? to_f32(row.q[v + j]) : 0.f;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < kLoads; ++e)
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) w[e][j] -= q[e][j];
+    }
+    if ((unsigned)(row.drafted - c * kChunk) < (unsigned)kChunk) {
+#pragma unroll
+        for (int e = 0; e < kLoads; ++e)
+#pragma unroll
+            for (int j = 0; j < kVec; ++j)
+                if (v0 + e * 32 * kVec + j == row.drafted) w[e][j] -= 1.f;
     }
 }
+
+// The cluster's barrier in two halves, so that what needs no other CTA runs between them.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 template <typename T, int kVec>
 __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_constant__ VerifyParams p) {
     constexpr int kWarps = kVerThreads / 32, kLoads = kChunk / (32 * kVec);
-    constexpr int kBatch = kVec == 1 ? 16 : 4;  // loads of a row in flight a lane
     extern __shared__ unsigned long long chunk_sum[];  // of this CTA's chunks
     __shared__ unsigned long long s_total, s_weight[kChunk + kChunk / 32];
     __shared__ int s_n;
@@ -176,42 +197,12 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
         unsigned long long mine = 0;
         for (int c = c0 + warp; c < c1; c += kWarps) {
             Digits d;
-            const int v0 = c * kChunk + lane * kVec;
-            const bool plain = (c + 1) * kChunk <= p.V && (unsigned)(row.drafted - c * kChunk) >= (unsigned)kChunk;
-            if (plain && row.q) {  // whole chunks: kBatch loads of each row in flight a lane
+            float w[kLoads][kVec];
+            load_chunk<T, kVec>(row, c, lane, p.V, w);
 #pragma unroll
-                for (int e0 = 0; e0 < kLoads; e0 += kBatch) {
-                    float w[kBatch][kVec], q[kBatch][kVec];
+            for (int e = 0; e < kLoads; ++e)
 #pragma unroll
-                    for (int e = 0; e < kBatch; ++e) {
-                        load_probs<T, kVec>(row.p + v0 + (e0 + e) * 32 * kVec, w[e]);
-                        load_probs<T, kVec>(row.q + v0 + (e0 + e) * 32 * kVec, q[e]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < kBatch; ++e)
-#pragma unroll
-                        for (int j = 0; j < kVec; ++j) d.add(w[e][j] - q[e][j]);
-                }
-            } else if (plain) {
-#pragma unroll
-                for (int e0 = 0; e0 < kLoads; e0 += kBatch) {
-                    float w[kBatch][kVec];
-#pragma unroll
-                    for (int e = 0; e < kBatch; ++e) load_probs<T, kVec>(row.p + v0 + (e0 + e) * 32 * kVec, w[e]);
-#pragma unroll
-                    for (int e = 0; e < kBatch; ++e)
-#pragma unroll
-                        for (int j = 0; j < kVec; ++j) d.add(w[e][j]);
-                }
-            } else {
-                float w[kLoads][kVec];
-#pragma unroll
-                for (int e = 0; e < kLoads; ++e) load_weights<T, kVec>(row, v0 + e * 32 * kVec, p.V, w[e]);
-#pragma unroll
-                for (int e = 0; e < kLoads; ++e)
-#pragma unroll
-                    for (int j = 0; j < kVec; ++j) d.add(w[e][j]);
-            }
+                for (int j = 0; j < kVec; ++j) d.add(w[e][j]);
             const uint64_t sum = warp_sum(d.total(kLoads * kVec));
             if (lane == 0) chunk_sum[c - c0] = sum;
             mine += sum;
@@ -226,8 +217,9 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
             if (q < rank) before += v;
             total += v;
         }
-        cluster.sync();  // nobody's total is read any more: it may be rewritten, and CTAs may end
+        cluster_arrive();  // has read the totals
         if (total != 0 || !residual) break;
+        cluster_wait();    // nobody reads this CTA's any more: it may be rewritten
         residual = false;  // no weight is positive after a rejection: the target's own
         row.q = nullptr;
         row.drafted = -1;
@@ -241,65 +233,67 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
             if (io.next_slots) io.next_slots[i] = io.write_slots[r];
         }
     }
-    if (warp != 0 || total == 0) return;
-    const double f = (double)sample * (double)total;
-    unsigned long long mark = f >= 1.0 ? (unsigned long long)f : 0ull;  // 0 for a NaN too
-    mark = min(mark, total - 1);
-    if (mark < before) return;
-    mark -= before;  // among this CTA's own chunks, if there at all
-    // the first chunk, then the first entry, whose running sum is over the mark
-    auto scan = [&](unsigned long long v) {  // inclusive over the lanes
+    auto draw = [&]() {  // one warp: the entry that holds the mark
+        const double f = (double)sample * (double)total;
+        unsigned long long mark = f >= 1.0 ? (unsigned long long)f : 0ull;  // 0 for a NaN too
+        mark = min(mark, total - 1);
+        if (mark < before) return;
+        mark -= before;  // among this CTA's own chunks, if there at all
+        // the first chunk, then the first entry, whose running sum is over the mark
+        auto scan = [&](unsigned long long v) {  // inclusive over the lanes
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long w = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += w;
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long w = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += w;
+            }
+            return v;
+        };
+        int hit = -1;
+        for (int c = 0; c < c1 - c0 && hit < 0; c += 32) {
+            const unsigned long long run = scan(c + lane < c1 - c0 ? chunk_sum[c + lane] : 0ull);
+            const unsigned over = __ballot_sync(0xffffffffu, run > mark);
+            if (over) {
+                const int l = __ffs(over) - 1;
+                const unsigned long long below = l ? __shfl_sync(0xffffffffu, run, l - 1) : 0ull;
+                hit = c + l;
+                mark -= below;
+            } else {
+                mark -= __shfl_sync(0xffffffffu, run, 31);
+            }
         }
-        return v;
+        if (hit < 0) return;  // a later CTA's
+        // The chunk's weights in the order of the vocabulary, 32 in a row a lane; a pad of one keeps the rows off each
+        // other's banks.
+        const int v0 = (c0 + hit) * kChunk;
+        float w[kLoads][kVec];
+        load_chunk<T, kVec>(row, c0 + hit, lane, p.V, w);
+#pragma unroll
+        for (int e = 0; e < kLoads; ++e)
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                Digits d;
+                d.add(w[e][j]);
+                const int v = (e * 32 + lane) * kVec + j;
+                s_weight[v + v / 32] = d.total(1);
+            }
+        __syncwarp();
+        unsigned long long sum = 0;
+#pragma unroll 8
+        for (int j = 0; j < 32; ++j) sum += s_weight[lane * 33 + j];
+        const unsigned long long run = scan(sum);
+        if (lane == __ffs(__ballot_sync(0xffffffffu, run > mark)) - 1) {
+            unsigned long long c = run - sum;
+            int v = 0;
+#pragma unroll 8
+            for (int j = 0; j < 32; ++j) {  // entries whose running sum is not over the mark
+                c += s_weight[lane * 33 + j];
+                v += c <= mark;
+            }
+            io.out_tokens[r] = v0 + lane * 32 + v;
+        }
     };
-    int hit = -1;
-    for (int c = 0; c < c1 - c0 && hit < 0; c += 32) {
-        const unsigned long long run = scan(c + lane < c1 - c0 ? chunk_sum[c + lane] : 0ull);
-        const unsigned over = __ballot_sync(0xffffffffu, run > mark);
-        if (over) {
-            const int l = __ffs(over) - 1;
-            const unsigned long long below = l ? __shfl_sync(0xffffffffu, run, l - 1) : 0ull;
-            hit = c + l;
-            mark -= below;
-        } else {
-            mark -= __shfl_sync(0xffffffffu, run, 31);
-        }
-    }
-    if (hit < 0) return;  // a later CTA's
-    // The chunk's weights in the order of the vocabulary, 32 in a row a lane; a pad of one keeps the rows off each
-    // other's banks.
-    const int v0 = (c0 + hit) * kChunk;
-    float w[kLoads][kVec];
-#pragma unroll
-    for (int e = 0; e < kLoads; ++e) load_weights<T, kVec>(row, v0 + (e * 32 + lane) * kVec, p.V, w[e]);
-#pragma unroll
-    for (int e = 0; e < kLoads; ++e)
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            Digits d;
-            d.add(w[e][j]);
-            const int v = (e * 32 + lane) * kVec + j;
-            s_weight[v + v / 32] = d.total(1);
-        }
-    __syncwarp();
-    unsigned long long sum = 0;
-#pragma unroll 8
-    for (int j = 0; j < 32; ++j) sum += s_weight[lane * 33 + j];
-    const unsigned long long run = scan(sum);
-    if (lane == __ffs(__ballot_sync(0xffffffffu, run > mark)) - 1) {
-        unsigned long long c = run - sum;
-        int v = 0;
-#pragma unroll 8
-        for (int j = 0; j < 32; ++j) {  // entries whose running sum is not over the mark
-            c += s_weight[lane * 33 + j];
-            v += c <= mark;
-        }
-        io.out_tokens[r] = v0 + lane * 32 + v;
-    }
+    if (warp == 0 && total != 0) draw();
+    cluster_wait();  // a CTA ends when nobody reads its total any more
 }
 
 template <typename T, int kVec>
