@@ -66,9 +66,17 @@ __device__ __forceinline__ float2 load_pair(const __nv_bfloat16 *p) {
     const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
-__device__ __forceinline__ void store_pair(float *p, float2 v) { *reinterpret_cast<float2 *>(p) = v; }
-__device__ __forceinline__ void store_pair(__nv_bfloat16 *p, float2 v) {
-    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
+// Predicated, so that a block of tokens stays one straight run of instructions.
+__device__ __forceinline__ void store_pair_if(bool on, float *p, float2 v) {
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %0, 0;\n @q st.global.v2.f32 [%1], {%2, %3};\n}" ::"r"((int)on), "l"(p),
+                 "f"(v.x), "f"(v.y)
+                 : "memory");
+}
+__device__ __forceinline__ void store_pair_if(bool on, __nv_bfloat16 *p, float2 v) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %0, 0;\n @q st.global.b32 [%1], %2;\n}" ::"r"((int)on), "l"(p),
+                 "r"(*reinterpret_cast<const uint32_t *>(&b))
+                 : "memory");
 }
 
 // Four neighbouring elements in registers.
@@ -119,6 +127,13 @@ struct Cfg {
         float2 yp[2][WARPS][TB][32];    // a block's partial sums, [token][lane]
     };
 };
+
+// Staged rows are 64 (bf16) or 128 (fp32) bytes apart, so the lanes of a warp that read neighbouring rows would meet in a
+// bank: rows whose number has the bit below set hold their two halves the other way round.
+template <typename T>
+__device__ __forceinline__ int swizzle(int row) {
+    return sizeof(T) == 2 ? (row & 2) * (kCh / 4) : (row & 1) * (kCh / 2);
+}
 
 template <int THREADS>
 __device__ __forceinline__ void cta_sync() {
@@ -206,29 +221,38 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
     if ((part > 0 && from >= all) || (kStates && ends)) return;  // no such segment; nobody needs its state
     auto tile_begin = [&](int k) { return k == 0 ? 0 : k * kTile - lead; };
     auto rows_of = [&](int k) { return min(len, (k + 1) * kTile - lead) - tile_begin(k); };
-    auto stage = [&](int k) {  // asynchronous copies of u, delta and z of tile k
-        const int t0 = tile_begin(k), n = rows_of(k), st = k % 3;
-        constexpr int E = 16 / sizeof(T);  // elements of a vector
+    // Asynchronous copies of u, delta and z of tile k; called for one tile after the other.
+    constexpr int E = 16 / sizeof(T), V = kCh / E;                  // elements of a vector, vectors of a row
+    constexpr int ROWS = THREADS / V, PASSES = (kTile + ROWS - 1) / ROWS;
+    const int sr = tid / V, sc = tid % V * E;                       // this thread's first row and column of a tile
+    const T *su = gu + (tile_begin(from) + sr) * s.us + sc, *sd = gd + (tile_begin(from) + sr) * s.ds + sc;
+    const T *sz = gz + (tile_begin(from) + sr) * s.zs + sc;
+    auto stage = [&](int k) {
+        const int n = rows_of(k), st = k % 3;
         if (p.vec) {
-            constexpr int V = kCh / E;     // vectors of a row
-            for (int q = tid; q < n * V; q += THREADS) {
-                const int r = q / V, col = q % V * E;
-                if (col >= width) continue;
-                const size_t t = t0 + r;
-                cp16(&sm.raw[st][0][r][col], gu + t * s.us + col);
-                cp16(&sm.raw[st][1][r][col], gd + t * s.ds + col);
-                if (!kStates && (kCommon || gz)) cp16(&sm.raw[st][2][r][col], gz + t * s.zs + col);
+#pragma unroll
+            for (int m = 0; m < PASSES; ++m) {
+                const int r = sr + m * ROWS;
+                if (r < n && sc < width) {
+                    T *dst = &sm.raw[st][0][r][sc ^ swizzle<T>(r)];
+                    cp16(dst, su + m * ROWS * s.us);
+                    cp16(dst + kTile * kCh, sd + m * ROWS * s.ds);
+                    if (!kStates && (kCommon || gz)) cp16(dst + 2 * kTile * kCh, sz + m * ROWS * s.zs);
+                }
             }
         } else {
             for (int q = tid; q < n * kCh; q += THREADS) {
                 const int r = q / kCh, col = q % kCh;
                 if (col >= width) continue;
-                const size_t t = t0 + r;
-                cp_elem(&sm.raw[st][0][r][col], gu + t * s.us + col);
-                cp_elem(&sm.raw[st][1][r][col], gd + t * s.ds + col);
-                if (!kStates && (kCommon || gz)) cp_elem(&sm.raw[st][2][r][col], gz + t * s.zs + col);
+                T *dst = &sm.raw[st][0][r][col ^ swizzle<T>(r)];
+                cp_elem(dst, su + (int64_t)(r - sr) * s.us + (col - sc));
+                cp_elem(dst + kTile * kCh, sd + (int64_t)(r - sr) * s.ds + (col - sc));
+                if (!kStates && (kCommon || gz)) cp_elem(dst + 2 * kTile * kCh, sz + (int64_t)(r - sr) * s.zs + (col - sc));
             }
         }
+        su += n * s.us;
+        sd += n * s.ds;
+        sz += n * s.zs;
         cp_commit();
     };
     Four<T> bq[IT], cq[IT];            // B and C of the next tile on their way
@@ -331,11 +355,12 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
 #pragma unroll
         for (int q = 0; q < OWN; ++q) {
             if (stage == 0) {
-                o.uv[q] = load_pair(r + q * kCh);
-                w.v[q] = load_pair(r + (kTile + q) * kCh);
+                const T *at = r + q * kCh + (c ^ swizzle<T>(l * OWN + q));  // blocks start at multiples of four rows
+                o.uv[q] = load_pair(at);
+                w.v[q] = load_pair(at + kTile * kCh);
                 w.v[q].x += bias.x;
                 w.v[q].y += bias.y;
-                if (gated) w.z[q] = load_pair(r + (2 * kTile + q) * kCh);
+                if (gated) w.z[q] = load_pair(at + 2 * kTile * kCh);
             } else if (stage == 1) {
                 if (softplus) w.e[q] = upk(softplus_exp(pk(w.v[q].x, w.v[q].y)));
                 if (gated) {
@@ -357,6 +382,9 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
             }
         }
     };
+    int yp_at[L];  // where a lane finds the parts of its first own token: its own column first, then the others'
+#pragma unroll
+    for (int e = 0; e < L; ++e) yp_at[e] = l * OWN * 32 + (lane ^ e * PW);
     // Outputs of the block computed before, from exchange buffer x, in two stages: the sums of the lane's own tokens,
     // then those of the `valid` first tokens to memory (the lane's first at dst).
     auto finish = [&](int stage, float2 (&out)[OWN], const Own &o, int x, T *dst, int valid) {
@@ -367,7 +395,7 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
                 f2 v = 0;
 #pragma unroll
                 for (int e = 0; e < L; ++e) {  // lane l starts with its own column: no two lanes in one bank
-                    const f2 w = *reinterpret_cast<const f2 *>(&sm.yp[x][warp][j][lane ^ e * PW]);
+                    const f2 w = *reinterpret_cast<const f2 *>(&sm.yp[x][warp][q][yp_at[e]]);
                     v = e ? add2(v, w) : w;
                 }
                 out[q] = upk(v);
@@ -379,7 +407,7 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
                 }
                 T *at = dst + (size_t)q * s.ys;
                 if (kCommon || p.y_pair) {
-                    if (j < valid && mine[1]) store_pair(at, v);
+                    store_pair_if(j < valid && mine[1], at, v);
                 } else {
                     if (j < valid && mine[0]) at[0] = from_f32<T>(v.x);
                     if (j < valid && mine[1]) at[1] = from_f32<T>(v.y);
@@ -399,7 +427,7 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
         else cp_wait<0>();
         cta_sync<THREADS>();
         int buf = from % 3;                // raw buffer of the tile at hand
-        auto raw_row = [&](int which) { return &sm.raw[which][0][l * OWN][c]; };
+        auto raw_row = [&](int which) { return &sm.raw[which][0][l * OWN][0]; };
         Own before = {}, now, next;        // the block computed last, the one at hand, the one prepared beside it
         {
             Steps w;
@@ -560,6 +588,9 @@ cudaError_t launch_k(const SelParams &p, cudaStream_t stream) {
                                               : launch_g<T, NP, L, false, false>(p, stream);
 }
 
+#ifndef SEL_L32
+#define SEL_L32 8
+#endif
 #ifndef SEL_L16
 #define SEL_L16 4
 #endif
@@ -569,7 +600,7 @@ cudaError_t launch(const SelParams &p, cudaStream_t stream) {
     if (p.s.N <= 4) return launch_k<T, 4, 2>(p, stream);
     if (p.s.N <= 8) return launch_k<T, 8, 2>(p, stream);
     if (p.s.N <= 16) return launch_k<T, 16, SEL_L16>(p, stream);
-    if (p.s.N <= 32) return launch_k<T, 32, 4>(p, stream);
+    if (p.s.N <= 32) return launch_k<T, 32, SEL_L32>(p, stream);
     if (p.s.N <= 64) return launch_k<T, 64, 8>(p, stream);
     if (p.s.N <= 128) return launch_k<T, 128, 8>(p, stream);
     return launch_k<T, 256, 8>(p, stream);

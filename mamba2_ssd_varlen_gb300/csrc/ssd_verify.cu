@@ -87,43 +87,40 @@ struct Row {
     int drafted;     // the token that 1 is taken off, or -1
 };
 
-// The weights of chunk c, kVec neighbouring ones a load, lane by lane; zeros past V.  Every load is issued before a
-// value is used.
-template <typename T, int kVec>
-__device__ __forceinline__ void load_chunk(const Row<T> &row, int c, int lane, int V,
-                                           float (&w)[kChunk / (32 * kVec)][kVec]) {
-    constexpr int kLoads = kChunk / (32 * kVec);
-    const int v0 = c * kChunk + lane * kVec;
-    float q[kLoads][kVec];
+// Loads e0 .. e0 + kE - 1 of chunk c's weights, kVec neighbouring ones a load, lane by lane; zeros past V.  Every load is
+// issued before a value is used.
+template <typename T, int kVec, int kE>
+__device__ __forceinline__ void load_part(const Row<T> &row, int c, int e0, int lane, int V, float (&w)[kE][kVec]) {
+    const int v0 = c * kChunk + (e0 * 32 + lane) * kVec;
+    auto fetch = [&](const T *p, float (&x)[kE][kVec]) {
+        if ((c + 1) * kChunk <= V) {
 #pragma unroll
-    for (int e = 0; e < kLoads; ++e) {
-        const int v = v0 + e * 32 * kVec;
-        if (v + kVec <= V) {
-            load_probs<T, kVec>(row.p + v, w[e]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) w[e][j] = v + j < V ? to_f32(row.p[v + j]) : 0.f;
+            for (int e = 0; e < kE; ++e) load_probs<T, kVec>(p + v0 + e * 32 * kVec, x[e]);
+            return;
         }
-    }
-    if (row.q) {
 #pragma unroll
-        for (int e = 0; e < kLoads; ++e) {
+        for (int e = 0; e < kE; ++e) {
             const int v = v0 + e * 32 * kVec;
             if (v + kVec <= V) {
-                load_probs<T, kVec>(row.q + v, q[e]);
+                load_probs<T, kVec>(p + v, x[e]);
             } else {
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) q[e][j] = v + j < V ? to_f32(row.q[v + j]) : 0.f;
+                for (int j = 0; j < kVec; ++j) x[e][j] = v + j < V ? to_f32(p[v + j]) : 0.f;
             }
         }
+    };
+    fetch(row.p, w);
+    if (row.q) {
+        float q[kE][kVec];
+        fetch(row.q, q);
 #pragma unroll
-        for (int e = 0; e < kLoads; ++e)
+        for (int e = 0; e < kE; ++e)
 #pragma unroll
             for (int j = 0; j < kVec; ++j) w[e][j] -= q[e][j];
     }
     if ((unsigned)(row.drafted - c * kChunk) < (unsigned)kChunk) {
 #pragma unroll
-        for (int e = 0; e < kLoads; ++e)
+        for (int e = 0; e < kE; ++e)
 #pragma unroll
             for (int j = 0; j < kVec; ++j)
                 if (v0 + e * 32 * kVec + j == row.drafted) w[e][j] -= 1.f;
@@ -137,6 +134,7 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 template <typename T, int kVec>
 __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_constant__ VerifyParams p) {
     constexpr int kWarps = kVerThreads / 32, kLoads = kChunk / (32 * kVec);
+    constexpr int kBatch = kVec == 1 ? 16 : 4;  // loads of a row in flight a lane
     extern __shared__ unsigned long long chunk_sum[];  // of this CTA's chunks
     __shared__ unsigned long long s_total, s_weight[kChunk + kChunk / 32];
     __shared__ int s_n;
@@ -197,12 +195,15 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
         unsigned long long mine = 0;
         for (int c = c0 + warp; c < c1; c += kWarps) {
             Digits d;
-            float w[kLoads][kVec];
-            load_chunk<T, kVec>(row, c, lane, p.V, w);
 #pragma unroll
-            for (int e = 0; e < kLoads; ++e)
+            for (int e0 = 0; e0 < kLoads; e0 += kBatch) {
+                float w[kBatch][kVec];
+                load_part<T, kVec, kBatch>(row, c, e0, lane, p.V, w);
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) d.add(w[e][j]);
+                for (int e = 0; e < kBatch; ++e)
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j) d.add(w[e][j]);
+            }
             const uint64_t sum = warp_sum(d.total(kLoads * kVec));
             if (lane == 0) chunk_sum[c - c0] = sum;
             mine += sum;
@@ -265,17 +266,20 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
         // The chunk's weights in the order of the vocabulary, 32 in a row a lane; a pad of one keeps the rows off each
         // other's banks.
         const int v0 = (c0 + hit) * kChunk;
-        float w[kLoads][kVec];
-        load_chunk<T, kVec>(row, c0 + hit, lane, p.V, w);
 #pragma unroll
-        for (int e = 0; e < kLoads; ++e)
+        for (int e0 = 0; e0 < kLoads; e0 += kBatch) {
+            float w[kBatch][kVec];
+            load_part<T, kVec, kBatch>(row, c0 + hit, e0, lane, p.V, w);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                Digits d;
-                d.add(w[e][j]);
-                const int v = (e * 32 + lane) * kVec + j;
-                s_weight[v + v / 32] = d.total(1);
-            }
+            for (int e = 0; e < kBatch; ++e)
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    Digits d;
+                    d.add(w[e][j]);
+                    const int v = ((e0 + e) * 32 + lane) * kVec + j;
+                    s_weight[v + v / 32] = d.total(1);
+                }
+        }
         __syncwarp();
         unsigned long long sum = 0;
 #pragma unroll 8
