@@ -61,6 +61,18 @@ __global__ void __launch_bounds__(kCsThreads) conv1d_step_kernel(const __grid_co
     const int i0 = (int)(blockIdx.x / p.tiles) * p.rb, count = min(p.rb, p.R - i0);
     const int c = ((int)(blockIdx.x % p.tiles) * kCsThreads + (int)threadIdx.x) * kN;
     const bool there = c < p.D;
+    float w[kN * W], bias[kN];
+#pragma unroll
+    for (int e = 0; e < kN; ++e) bias[e] = there && io.bias ? io.bias[c + e] : 0.f;
+    if constexpr (kN % 4 == 0) {
+#pragma unroll
+        for (int e = 0; e < kN * W; e += 4)
+            *reinterpret_cast<float4 *>(w + e) = there ? *reinterpret_cast<const float4 *>(io.weight + (size_t)c * W + e)
+                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kN * W; ++e) w[e] = there ? io.weight[(size_t)c * W + e] : 0.f;
+    }
     // lane q: the window and the read slot of request i0 + q
     int ma = 0, mb = 0, ms = -1;
     if (lane < count) {
@@ -95,18 +107,6 @@ __global__ void __launch_bounds__(kCsThreads) conv1d_step_kernel(const __grid_co
         if (b > a && there) in.load(x + (size_t)a * p.D);
     };
     fetch(0);
-    float w[kN * W], bias[kN];
-#pragma unroll
-    for (int e = 0; e < kN; ++e) bias[e] = there && io.bias ? io.bias[c + e] : 0.f;
-    if constexpr (kN % 4 == 0) {
-#pragma unroll
-        for (int e = 0; e < kN * W; e += 4)
-            *reinterpret_cast<float4 *>(w + e) = there ? *reinterpret_cast<const float4 *>(io.weight + (size_t)c * W + e)
-                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-    } else {
-#pragma unroll
-        for (int e = 0; e < kN * W; ++e) w[e] = there ? io.weight[(size_t)c * W + e] : 0.f;
-    }
     for (int q = 0; q < count; ++q) {
         const int a = __shfl_sync(0xffffffffu, ma, q), b = __shfl_sync(0xffffffffu, mb, q);
         T win[W][kN];

@@ -77,6 +77,24 @@ __global__ void __launch_bounds__(kStepThreads, QL == 32 && NV == 2 ? 2 : STEP_M
     const int d0 = g * dg + tile % per_group * CW, width = min(CW, (g + 1) * dg - d0);
     const size_t dn = (size_t)s.D * s.N;
 
+    // channel k of the group: gr + GR k, so that a warp's access covers neighbouring channels
+    const size_t at0 = (size_t)(d0 + gr) * s.N + 4 * l;  // the lane's first state
+    auto quad = [&](int k, int v, int &n) {  // quad (k, v) from there on, and how many of it there are
+        const int n0 = 4 * (l + QL * v);
+        n = kExact ? 4 : gr + GR * k < width ? min(4, s.N - n0) : 0;
+        return kExact ? (size_t)(GR * k * 4 * QL * NV + 4 * QL * v) : (size_t)GR * k * s.N + 4 * QL * v;
+    };
+    float4 A[CPG][NV];
+#pragma unroll
+    for (int k = 0; k < CPG; ++k)
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            int n;
+            const size_t at = quad(k, v, n);
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (n > 0) x = kExact || p.vec ? four(io.A + at0 + at) : some(io.A + at0 + at, n);
+            A[k][v] = x;
+        }
     // lane q: the window and the read slot of request i0 + q
     int ma = 0, mb = 0, ms = -1;
     if (lane < count) {
@@ -92,13 +110,6 @@ __global__ void __launch_bounds__(kStepThreads, QL == 32 && NV == 2 ? 2 : STEP_M
             ms = -1;
         }
     }
-    // channel k of the group: gr + GR k, so that a warp's access covers neighbouring channels
-    const size_t at0 = (size_t)(d0 + gr) * s.N + 4 * l;  // the lane's first state
-    auto quad = [&](int k, int v, int &n) {  // quad (k, v) from there on, and how many of it there are
-        const int n0 = 4 * (l + QL * v);
-        n = kExact ? 4 : gr + GR * k < width ? min(4, s.N - n0) : 0;
-        return kExact ? (size_t)(GR * k * 4 * QL * NV + 4 * QL * v) : (size_t)GR * k * s.N + 4 * QL * v;
-    };
     auto stage = [&](int q) {  // the states of request i0 + q, on their way
         const int slot = q < count ? __shfl_sync(0xffffffffu, ms, q) : -1;
         const float *src = io.state_pool + (size_t)max(slot, 0) * dn + at0;
@@ -127,17 +138,11 @@ __global__ void __launch_bounds__(kStepThreads, QL == 32 && NV == 2 ? 2 : STEP_M
 #pragma unroll
     for (int q = 0; q < kRing - 1; ++q) stage(q);
 
-    float4 A[CPG][NV];
 #pragma unroll
     for (int k = 0; k < CPG; ++k)
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            int n;
-            const size_t at = quad(k, v, n);
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (n > 0) x = kExact || p.vec ? four(io.A + at0 + at) : some(io.A + at0 + at, n);
-            A[k][v] = make_float4(x.x * kLog2e, x.y * kLog2e, x.z * kLog2e, x.w * kLog2e);
-        }
+        for (int v = 0; v < NV; ++v)
+            A[k][v] = make_float4(A[k][v].x * kLog2e, A[k][v].y * kLog2e, A[k][v].z * kLog2e, A[k][v].w * kLog2e);
     // the lane's own channel (lanes past CPG have none)
     const int own = gr + GR * l, d = d0 + own;
     const bool mine = l < CPG && own < width;
