@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
                     }
 #pragma unroll
                     for (int q = 0; q < NS; ++q) {
-                        const float2 x = upk(mul2(pk(dd.x, dd.y), pk(A[q].x, A[q].y)));
+                        const float2 x = upk(fma2(pk(dd.x, dd.y), pk(A[q].x, A[q].y), pk(kDecayShift, kDecayShift)));
                         h[q].x = fmaf(ex2f(x.x), h[q].x, dd.z * bc[q].x);
                         h[q].y = fmaf(ex2f(x.y), h[q].y, dd.w * bc[q].x);
                         if (!kStates) {

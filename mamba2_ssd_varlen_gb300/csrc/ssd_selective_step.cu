@@ -226,10 +226,10 @@ __global__ void __launch_bounds__(kStepThreads, QL == 32 && NV == 2 ? 2 : STEP_M
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
                     float4 &x = h[k][v];
-                    x.x = fmaf(ex2f(dk * A[k][v].x), x.x, uk * now.b[v].x);
-                    x.y = fmaf(ex2f(dk * A[k][v].y), x.y, uk * now.b[v].y);
-                    x.z = fmaf(ex2f(dk * A[k][v].z), x.z, uk * now.b[v].z);
-                    x.w = fmaf(ex2f(dk * A[k][v].w), x.w, uk * now.b[v].w);
+                    x.x = fmaf(ex2f(fmaf(dk, A[k][v].x, kDecayShift)), x.x, uk * now.b[v].x);
+                    x.y = fmaf(ex2f(fmaf(dk, A[k][v].y, kDecayShift)), x.y, uk * now.b[v].y);
+                    x.z = fmaf(ex2f(fmaf(dk, A[k][v].z, kDecayShift)), x.z, uk * now.b[v].z);
+                    x.w = fmaf(ex2f(fmaf(dk, A[k][v].w, kDecayShift)), x.w, uk * now.b[v].w);
                     acc[k] = fmaf(x.x, now.c[v].x, acc[k]);
                     acc[k] = fmaf(x.y, now.c[v].y, acc[k]);
                     acc[k] = fmaf(x.z, now.c[v].z, acc[k]);
