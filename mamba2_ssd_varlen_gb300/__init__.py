@@ -624,9 +624,15 @@ class _Prepared:
         _check_plain(cu, (self.dims.R + 1,), torch.int32, "cu_seqlens")
         self._name, self._fn = name, fn
         self._args = (ctypes.byref(self.dims), _ptr(cu), ctypes.byref(self.io))
+        # the current stream's handle without an object for it, where this torch has that (a call's other
+        # half of host time)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._raw = raw if self.stream is None and cu.is_cuda else None
+        self._device = cu.device.index
 
     def __call__(self):
-        rc = self._fn(*self._args, _stream(self.stream))
+        stream = _stream(self.stream) if self._raw is None else c_vp(self._raw(self._device))
+        rc = self._fn(*self._args, stream)
         if rc != 0:
             raise SsdError(rc, self._name)
         return self

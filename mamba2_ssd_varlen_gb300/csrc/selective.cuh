@@ -1,4 +1,4 @@
-// selective.cuh -- what the selective scan's two kernels (prefill and windows) share.
+// selective.cuh -- what the selective scan's kernels (prefill and windows) and entry points share.
 #pragma once
 
 #include "ssd_internal.cuh"
@@ -54,5 +54,31 @@ inline int sel_shape(const ssd_selective_dims *d, bool has_z, SelShape *s) {
 }
 
 inline bool sel_aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+// ---- the prefill's cut into CTAs ---------------------------------------------
+constexpr int kTile = 16;  // tokens staged at a time
+constexpr int kCh = 32;    // channels of a CTA
+constexpr int kPairs = kCh / 2;
+constexpr int kMaxOrdered = 128;  // requests that are put in order of their lengths
+
+struct SelParams {
+    SelShape s;
+    const int32_t *cu;
+    ssd_selective_io io;
+    int32_t tiles;   // channel tiles of a request: G * ceil((D / G) / 32)
+    int32_t vec;     // u, delta, z: every tile row of a CTA starts on a 16-byte boundary
+    int32_t bc_vec;  // B, C: every four states of a row start on a boundary of four elements
+    int32_t y_pair;  // y: every pair of channels starts on a boundary of two elements
+    int32_t ordered; // CTAs take the requests longest first
+    int32_t seg;     // tiles of a segment where requests are split over the time; 0: not split
+    float *seg_state;  // (segment places, D, N): the state after a segment that entered it with zeros
+    float *seg_steps;  // (segment places, D): the sum of its steps
+};
+
+// Places of segments where requests are split over the time (selective_scan.cuh).
+inline int64_t seg_places(int64_t T, int64_t R, int64_t seg) { return (T + kTile * R) / (kTile * seg) + R; }
+
+cudaError_t launch_selective_bf16(const SelParams &p, cudaStream_t stream);
+cudaError_t launch_selective_f32(const SelParams &p, cudaStream_t stream);
 
 }  // namespace ssd

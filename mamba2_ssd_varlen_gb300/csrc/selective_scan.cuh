@@ -1,0 +1,606 @@
+// selective_scan.cuh -- the kernel of the selective-scan (S6) prefill and its launch, for one
+// element type a translation unit.
+//
+//   dt' = softplus(delta[t,d] + bias[d])
+//   h[d,n] <- exp(dt' A[d,n]) h[d,n] + dt' u[t,d] B[t,g,n]
+//   y[t,d] = (sum_n C[t,g,n] h[d,n] + D[d] u[t,d]) silu(z[t,d])
+//
+// Every (token, channel, state) costs an exponential and four fp32 operations on the
+// general pipe (two products, two multiply-adds); no part of it is a matrix product,
+// because the decay differs for every channel and state.  The kernel is bound by
+// instruction issue and those pipes, not by memory, so its shape is chosen to spend as
+// few other instructions as possible:
+//   - a CTA walks the tokens of one request for 32 channels of one group; a lane holds
+//     two neighbouring channels as one packed fp32 pair (two multiply-adds an issue slot,
+//     and u, delta, z and y move as pairs) and NP / L of their states, L lanes a pair;
+//   - u, delta and z arrive by tiles of 16 tokens through asynchronous copies, two tiles
+//     ahead; B and C through registers, a tile ahead, laid out in shared memory as the
+//     (B, B, C, C) that a packed pair multiplies by: one 16-byte load a state;
+//   - softplus, u dt', the skip term and the gate are computed by the L lanes of a pair
+//     for different tokens, and exchanged through shared memory.  They, and the sums over
+//     the L lanes, belong to the blocks of TB tokens after and before the one whose
+//     recurrence runs beside them, so that their latency hides behind it.
+#pragma once
+
+#include "async_copy.cuh"
+#include "pdl.cuh"
+#include "selective.cuh"
+#include "special.cuh"
+
+namespace ssd {
+
+template <typename T>
+__device__ __forceinline__ void cp_elem(T *smem, const T *gmem) {
+    if constexpr (sizeof(T) == 4) cp4(smem, gmem);
+    else *smem = *gmem;  // two bytes: no asynchronous copy is that small
+}
+
+template <int THREADS>
+__device__ __forceinline__ void cta_sync() {
+    if constexpr (THREADS <= 32) __syncwarp();
+    else __syncthreads();
+}
+
+// The request whose length comes `place`-th, the longest first (equal ones by their number): the last CTAs to start are
+// then short ones.  kMaxOrdered + 1 words of shared memory.
+template <int THREADS>
+__device__ __forceinline__ int longest_first(const SelParams &p, int place, int *w) {
+    for (int q = threadIdx.x; q < p.s.R; q += THREADS) w[q] = p.cu[q + 1] - p.cu[q];
+    cta_sync<THREADS>();
+    for (int q = threadIdx.x; q < p.s.R; q += THREADS) {
+        int rank = 0;
+        for (int j = 0; j < p.s.R; ++j) rank += w[j] > w[q] || (w[j] == w[q] && j < q);
+        if (rank == place) w[kMaxOrdered] = q;
+    }
+    cta_sync<THREADS>();
+    const int i = w[kMaxOrdered];
+    cta_sync<THREADS>();  // the words are free
+    return i;
+}
+
+template <bool v>
+struct Flag {
+    static constexpr bool value = v;
+};
+
+// Two neighbouring elements to and from fp32.
+__device__ __forceinline__ float2 load_pair(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+__device__ __forceinline__ float2 load_pair(const __nv_bfloat16 *p) {
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+// Predicated, so that a block of tokens stays one straight run of instructions.
+__device__ __forceinline__ void store_pair_if(bool on, float *p, float2 v) {
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %0, 0;\n @q st.global.v2.f32 [%1], {%2, %3};\n}" ::"r"((int)on), "l"(p),
+                 "f"(v.x), "f"(v.y)
+                 : "memory");
+}
+__device__ __forceinline__ void store_pair_if(bool on, __nv_bfloat16 *p, float2 v) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %0, 0;\n @q st.global.b32 [%1], %2;\n}" ::"r"((int)on), "l"(p),
+                 "r"(*reinterpret_cast<const uint32_t *>(&b))
+                 : "memory");
+}
+
+// Four neighbouring elements in registers.
+template <typename T>
+struct Four;
+template <>
+struct Four<float> {
+    float4 v;
+    __device__ __forceinline__ void load(const float *p) { v = *reinterpret_cast<const float4 *>(p); }
+    __device__ __forceinline__ void set(int j, float x) { (&v.x)[j] = x; }
+    __device__ __forceinline__ float4 get() const { return v; }
+};
+template <>
+struct Four<__nv_bfloat16> {
+    uint2 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void set(int j, __nv_bfloat16 x) {
+        const uint32_t b = *reinterpret_cast<const unsigned short *>(&x);
+        uint32_t &w = j < 2 ? v.x : v.y;
+        w = j & 1 ? (w & 0xFFFFu) | b << 16 : (w & 0xFFFF0000u) | b;
+    }
+    __device__ __forceinline__ float4 get() const {
+        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                           __uint_as_float(v.y & 0xFFFF0000u));
+    }
+};
+
+// L lanes a pair of channels (lane = l * PW + pair in a warp of PW pairs); blocks of TB
+// tokens, OWN of them each lane's own.
+template <typename T, int NP, int L>
+struct Cfg {
+    static constexpr int NS = NP / L;              // states of a lane
+    static constexpr int PW = 32 / L;              // pairs of a warp
+    static constexpr int OWN = L < 4 ? 4 / L : 1;
+    static constexpr int TB = OWN * L;
+    static constexpr int THREADS = kPairs * L;
+    static constexpr int WARPS = (THREADS + 31) / 32;
+    static constexpr int QUADS = kTile * NP / 4;   // (row, four states) of a tile of B or C
+    static constexpr int IT = (QUADS + THREADS - 1) / THREADS;
+    // registers a thread: what the states, the decay rates and a block's work need without spilling
+    static constexpr int REGS = NS <= 4 ? 160 : NS <= 8 ? 224 : 255;
+    static constexpr int MIN = 65536 / (THREADS * REGS) > 1 ? 65536 / (THREADS * REGS) : 1;
+    static_assert(NS >= 1 && kTile % TB == 0 && L <= 16, "whole blocks, a pair inside a warp");
+    struct Smem {
+        T raw[3][3][kTile][kCh];        // u, delta, z of the tile at hand, the next and the one in flight
+        float2 f[2][kTile][NP];         // (B, C) of the tile at hand and the next; zeros past N
+        float4 dd[2][WARPS][TB][PW];    // dt' and dt' u of each pair: the block at hand and the next
+        float2 yp[2][WARPS][TB][32];    // a block's partial sums, [token][lane]
+    };
+};
+
+// Staged rows are 64 (bf16) or 128 (fp32) bytes apart, so the lanes of a warp that read neighbouring rows would meet in a
+// bank: rows whose number has the bit below set hold their two halves the other way round.
+template <typename T>
+__device__ __forceinline__ int swizzle(int row) {
+    return sizeof(T) == 2 ? (row & 2) * (kCh / 4) : (row & 1) * (kCh / 2);
+}
+
+// Requests split over the time: request i's segments sit at places seg_place(i), seg_place(i) + 1, ...; it has at most
+// (length + 15) / (16 seg) + 1 of them, so that the next request's first place is past its last, and a place's request is
+// found by a binary search in cu_seqlens alone.
+__device__ __forceinline__ int seg_place(const SelParams &p, int i) {
+    return (int)(((int64_t)p.cu[i] + (int64_t)kTile * i) / ((int64_t)kTile * p.seg)) + i;
+}
+__device__ __forceinline__ int seg_request(const SelParams &p, int place) {
+    int lo = 0, hi = p.s.R;  // seg_place(lo) <= place, the answer in [lo, hi)
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (seg_place(p, mid) <= place) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// kCommon: softplus, a gate, and pairs of y on their boundaries (what a layer has); else these are looked up.
+// kStates: only the states that segments leave behind, from zeros; no outputs.
+template <typename T, int NP, int L, bool kCommon, bool kStates>
+__global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kernel(const __grid_constant__ SelParams p) {
+    using K = Cfg<T, NP, L>;
+    constexpr int NS = K::NS, PW = K::PW, OWN = K::OWN, TB = K::TB, THREADS = K::THREADS, IT = K::IT;
+    extern __shared__ __align__(16) uint8_t sel_smem[];
+    typename K::Smem &sm = *reinterpret_cast<typename K::Smem *>(sel_smem);
+    pdl_wait();
+    const SelShape &s = p.s;
+    const ssd_selective_io &io = p.io;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int l = lane / PW, pr = lane % PW;       // this lane's share of the states, its pair in the warp
+    const int c = (warp * PW + pr) * 2;            // the pair's first channel in the tile
+    const int tile = (int)(blockIdx.x % p.tiles);
+    int i = (int)(blockIdx.x / p.tiles), place = i;
+    if (p.ordered) i = longest_first<THREADS>(p, place, reinterpret_cast<int *>(sel_smem));
+    if (p.seg) {
+        i = seg_request(p, place);
+        if (blockIdx.x == 0) {  // the places of a wrong cu_seqlens may leave out requests: all are looked at here
+            for (int q = tid; q < s.R; q += THREADS)
+                if (p.cu[q + 1] < p.cu[q] || (q == 0 && p.cu[0] != 0) || (q == s.R - 1 && p.cu[s.R] != s.T))
+                    atomicOr(io.device_err, SSD_DEVERR_CU_SEQLENS);
+        }
+    }
+    const int dg = s.D / s.G, per_group = p.tiles / s.G;
+    const int g = tile / per_group, off = (tile % per_group) * kCh;
+    const int width = min(kCh, dg - off);          // channels of this CTA
+    const int d0 = g * dg + off, d = d0 + c;
+    const bool mine[2] = {c < width, c + 1 < width};
+
+    const int64_t a = p.cu[i], b = p.cu[i + 1];
+    if (b < a || a < 0 || b > s.T || (i == 0 && a != 0) || (i == s.R - 1 && b != s.T)) {
+        if (tile == 0 && tid == 0) atomicOr(io.device_err, SSD_DEVERR_CU_SEQLENS);
+        return;
+    }
+    const int part = p.seg ? place - seg_place(p, i) : 0;  // the segment of the request
+    const bool first = tile == 0 && tid == 0;
+    const int len = (int)(b - a);
+    int done = 0;
+    bool table = io.block_table != nullptr;
+    if (table && io.num_computed) {
+        done = io.num_computed[i];
+        if (done < 0 || (int64_t)done + len > 0x7fffffffLL) {
+            if (first) atomicOr(io.device_err, SSD_DEVERR_NUM_COMPUTED);
+            table = false;
+            done = 0;
+        }
+    }
+
+    const T *gu = static_cast<const T *>(io.u) + a * s.us + d0, *gd = static_cast<const T *>(io.delta) + a * s.ds + d0;
+    const T *gz = !kStates && (kCommon || io.z) ? static_cast<const T *>(io.z) + a * s.zs + d0 : nullptr;
+    const T *gb = static_cast<const T *>(io.B) + a * s.bs + (size_t)g * s.N;
+    const T *gc = static_cast<const T *>(io.C) + a * s.cs + (size_t)g * s.N;
+    T *gy = static_cast<T *>(io.y) + a * s.ys + d;
+
+    // Tiles end at absolute multiples of kTile where block states are kept, so that a boundary ends its tile.
+    const int lead = table ? done % kTile : 0;
+    const int all = (lead + len + kTile - 1) / kTile;     // tiles of the request
+    const int from = part * p.seg, tiles = p.seg ? min(all, from + p.seg) : all;  // of this segment: from .. tiles - 1
+    const bool ends = tiles == all;
+    if ((part > 0 && from >= all) || (kStates && ends)) return;  // no such segment; nobody needs its state
+    auto tile_begin = [&](int k) { return k == 0 ? 0 : k * kTile - lead; };
+    auto rows_of = [&](int k) { return min(len, (k + 1) * kTile - lead) - tile_begin(k); };
+    // Asynchronous copies of u, delta and z of tile k; called for one tile after the other.
+    constexpr int E = 16 / sizeof(T), V = kCh / E;                  // elements of a vector, vectors of a row
+    constexpr int ROWS = THREADS / V, PASSES = (kTile + ROWS - 1) / ROWS;
+    const int sr = tid / V, sc = tid % V * E;                       // this thread's first row and column of a tile
+    const T *su = gu + (tile_begin(from) + sr) * s.us + sc, *sd = gd + (tile_begin(from) + sr) * s.ds + sc;
+    const T *sz = gz + (tile_begin(from) + sr) * s.zs + sc;
+    auto stage = [&](int k) {
+        const int n = rows_of(k), st = k % 3;
+        if (p.vec) {
+#pragma unroll
+            for (int m = 0; m < PASSES; ++m) {
+                const int r = sr + m * ROWS;
+                if (r < n && sc < width) {
+                    T *dst = &sm.raw[st][0][r][sc ^ swizzle<T>(r)];
+                    cp16(dst, su + m * ROWS * s.us);
+                    cp16(dst + kTile * kCh, sd + m * ROWS * s.ds);
+                    if (!kStates && (kCommon || gz)) cp16(dst + 2 * kTile * kCh, sz + m * ROWS * s.zs);
+                }
+            }
+        } else {
+            for (int q = tid; q < n * kCh; q += THREADS) {
+                const int r = q / kCh, col = q % kCh;
+                if (col >= width) continue;
+                T *dst = &sm.raw[st][0][r][col ^ swizzle<T>(r)];
+                cp_elem(dst, su + (int64_t)(r - sr) * s.us + (col - sc));
+                cp_elem(dst + kTile * kCh, sd + (int64_t)(r - sr) * s.ds + (col - sc));
+                if (!kStates && (kCommon || gz)) cp_elem(dst + 2 * kTile * kCh, sz + (int64_t)(r - sr) * s.zs + (col - sc));
+            }
+        }
+        su += n * s.us;
+        sd += n * s.ds;
+        sz += n * s.zs;
+        cp_commit();
+    };
+    Four<T> bq[IT], cq[IT];            // B and C of the next tile on their way
+    auto fetch_bc = [&](int k) {
+        const int t0 = tile_begin(k), n = rows_of(k);
+#pragma unroll
+        for (int q = 0; q < IT; ++q) {
+            const int e = tid + q * THREADS, r = e / (NP / 4), n4 = e % (NP / 4) * 4;
+            bq[q] = {}, cq[q] = {};
+            if (e >= K::QUADS || r >= n || n4 >= s.N) continue;
+            const T *sb = gb + (size_t)(t0 + r) * s.bs + n4, *sc = gc + (size_t)(t0 + r) * s.cs + n4;
+            if (p.bc_vec) {
+                bq[q].load(sb);
+                cq[q].load(sc);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (n4 + j < s.N) {
+                        bq[q].set(j, sb[j]);
+                        cq[q].set(j, sc[j]);
+                    }
+            }
+        }
+    };
+    auto widen_bc = [&](int k) {
+#pragma unroll
+        for (int q = 0; q < IT; ++q) {
+            const int e = tid + q * THREADS, r = e / (NP / 4), n4 = e % (NP / 4) * 4;
+            if (e >= K::QUADS) continue;
+            const float4 bv = bq[q].get(), cv = cq[q].get();
+            float4 *dst = reinterpret_cast<float4 *>(&sm.f[k & 1][r][n4]);
+            dst[0] = make_float4(bv.x, cv.x, bv.y, cv.y);
+            dst[1] = make_float4(bv.z, cv.z, bv.w, cv.w);
+        }
+    };
+
+    if (tiles > from && len > 0) {  // the first copies: what follows up to the first tile runs beside them
+        stage(from);
+        if (tiles > from + 1) stage(from + 1);
+        fetch_bc(from);
+    }
+
+    // The lane's states and decay rates (zeros past N and past the width: they stay zero).
+    const size_t dn = (size_t)s.D * s.N, row = (size_t)d * s.N;
+    const int n0 = l * NS;
+    float2 h[NS], A[NS];
+    {
+        const float *src = nullptr;
+        if (!kStates && io.init_slots) {
+            const int slot = io.init_slots[i];
+            if (slot >= s.num_slots) {
+                if (first) atomicOr(io.device_err, SSD_DEVERR_INIT_SLOT);
+            } else if (slot >= 0) {
+                src = io.state_pool + (size_t)slot * dn + row;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+            float hv[2], av[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const bool ok = mine[e] && n0 + k < s.N;
+                const size_t at = (size_t)e * s.N + n0 + k;
+                hv[e] = ok && src ? src[at] : 0.f;
+                av[e] = ok ? io.A[row + at] * kLog2e : 0.f;
+            }
+            h[k] = make_float2(hv[0], hv[1]);
+            A[k] = make_float2(av[0], av[1]);
+        }
+    }
+    if (!kStates && part > 0) {  // through the request's segments before this one
+        for (int q = place - part; q < place; ++q) {
+            const float *st = p.seg_steps + (size_t)q * s.D + d, *sv = p.seg_state + (size_t)q * dn + row;
+            const float2 steps = make_float2(mine[0] ? st[0] : 0.f, mine[1] ? st[1] : 0.f);
+#pragma unroll
+            for (int k = 0; k < NS; ++k) {
+                const bool ok = n0 + k < s.N;
+                h[k].x = fmaf(ex2f(steps.x * A[k].x), h[k].x, ok && mine[0] ? sv[n0 + k] : 0.f);
+                h[k].y = fmaf(ex2f(steps.y * A[k].y), h[k].y, ok && mine[1] ? sv[s.N + n0 + k] : 0.f);
+            }
+        }
+    }
+    auto two = [&](const float *v) { return make_float2(v && mine[0] ? v[d] : 0.f, v && mine[1] ? v[d + 1] : 0.f); };
+    const float2 bias = two(io.delta_bias), skip = two(io.D);
+    auto put = [&](float *base) {
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+            if (n0 + k < s.N) {
+                if (mine[0]) base[row + n0 + k] = h[k].x;
+                if (mine[1]) base[row + s.N + n0 + k] = h[k].y;
+            }
+        }
+    };
+
+    // A lane's own tokens of a block on their way from the staged rows to the exchange buffer (`steps`), and what it
+    // keeps of them until their sums are there.
+    struct Own {
+        float2 uv[OWN], gate[OWN];
+    };
+    struct Steps {
+        float2 v[OWN], e[OWN], r[OWN], z[OWN], ze[OWN];
+    };
+    const bool softplus = kCommon || s.softplus, gated = !kStates && (kCommon || gz != nullptr);
+    // Four stages, each taking up what the special-function unit gave the one before it.
+    auto prepare = [&](int stage, Own &o, Steps &w, const T *r, int x) {
+#pragma unroll
+        for (int q = 0; q < OWN; ++q) {
+            if (stage == 0) {
+                const T *at = r + q * kCh + (c ^ swizzle<T>(l * OWN + q));  // blocks start at multiples of four rows
+                o.uv[q] = load_pair(at);
+                w.v[q] = load_pair(at + kTile * kCh);
+                w.v[q].x += bias.x;
+                w.v[q].y += bias.y;
+                if (gated) w.z[q] = load_pair(at + 2 * kTile * kCh);
+            } else if (stage == 1) {
+                if (softplus) w.e[q] = upk(softplus_exp(pk(w.v[q].x, w.v[q].y)));
+                if (gated) {
+                    const float2 x = upk(mul2(pk(w.z[q].x, w.z[q].y), pk(-kLog2e, -kLog2e)));
+                    w.ze[q] = make_float2(ex2f(x.x), ex2f(x.y));
+                }
+            } else if (stage == 2) {
+                if (softplus) w.r[q] = make_float2(rcpf(w.e[q].x + 2.f), rcpf(w.e[q].y + 2.f));
+                if (gated) o.gate[q] = make_float2(rcpf(1.f + w.ze[q].x), rcpf(1.f + w.ze[q].y));
+            } else {
+                if (softplus)
+                    w.v[q] = upk(softplus_end(pk(w.v[q].x, w.v[q].y), pk(w.e[q].x, w.e[q].y), pk(w.r[q].x, w.r[q].y)));
+                if (gated) {
+                    o.gate[q].x *= w.z[q].x;
+                    o.gate[q].y *= w.z[q].y;
+                }
+                sm.dd[x][warp][l * OWN + q][pr] =
+                    make_float4(w.v[q].x, w.v[q].y, w.v[q].x * o.uv[q].x, w.v[q].y * o.uv[q].y);
+            }
+        }
+    };
+    int yp_at[L];  // where a lane finds the parts of its first own token: its own column first, then the others'
+#pragma unroll
+    for (int e = 0; e < L; ++e) yp_at[e] = l * OWN * 32 + (lane ^ e * PW);
+    // Outputs of the block computed before, from exchange buffer x, in two stages: the sums of the lane's own tokens,
+    // then those of the `valid` first tokens to memory (the lane's first at dst).
+    auto finish = [&](int stage, float2 (&out)[OWN], const Own &o, int x, T *dst, int valid) {
+#pragma unroll
+        for (int q = 0; q < OWN; ++q) {
+            const int j = l * OWN + q;
+            if (stage == 0) {
+                f2 v = 0;
+#pragma unroll
+                for (int e = 0; e < L; ++e) {  // lane l starts with its own column: no two lanes in one bank
+                    const f2 w = *reinterpret_cast<const f2 *>(&sm.yp[x][warp][0][0] + q * 32 + yp_at[e]);
+                    v = e ? add2(v, w) : w;
+                }
+                out[q] = upk(v);
+            } else {
+                float2 v = make_float2(fmaf(skip.x, o.uv[q].x, out[q].x), fmaf(skip.y, o.uv[q].y, out[q].y));
+                if (gated) {
+                    v.x *= o.gate[q].x;
+                    v.y *= o.gate[q].y;
+                }
+                T *at = dst + (size_t)q * s.ys;
+                if (kCommon || p.y_pair) {
+                    store_pair_if(j < valid && mine[1], at, v);
+                } else {
+                    if (j < valid && mine[0]) at[0] = from_f32<T>(v.x);
+                    if (j < valid && mine[1]) at[1] = from_f32<T>(v.y);
+                }
+            }
+        }
+    };
+
+    // Tile k is computed while tile k + 1 (landed) is prepared for and tile k + 2 is in flight.
+    float2 steps = make_float2(0.f, 0.f);  // their sum over the segment
+    if (tiles > from && len > 0) {
+        widen_bc(from);
+        if (tiles > from + 1) cp_wait<1>();
+        else cp_wait<0>();
+        cta_sync<THREADS>();
+        int buf = from % 3;                // raw buffer of the tile at hand
+        auto raw_row = [&](int which) { return &sm.raw[which][0][l * OWN][0]; };
+        Own before = {}, now, next;        // the block computed last, the one at hand, the one prepared beside it
+        {
+            Steps w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) prepare(e, now, w, raw_row(buf), 0);
+        }
+        T *yp = gy + ((int64_t)tile_begin(from) + l * OWN - TB) * s.ys;  // y of the lane's first token in the block before
+        int before_valid = 0;                         // and how many of that block's tokens there are
+        const int64_t y_step = (int64_t)TB * s.ys;
+        // One block of tile k: the recurrence of its tokens, and between them, a stage at a time, the steps of the next
+        // block (rows from r on) and the outputs of the one before.  x: the exchange buffer of this block.
+        auto block = [&](const float2 *f, const T *r, int x, int valid, auto full) {
+            Steps w;
+            float2 acc[TB], out[OWN], sum = make_float2(0.f, 0.f);
+            if (!kStates) finish(0, out, before, x ^ 1, yp, before_valid);
+            prepare(0, next, w, r, x ^ 1);
+#pragma unroll
+            for (int j = 0; j < TB; ++j) {
+                acc[j] = make_float2(0.f, 0.f);
+                if (full.value || j < valid) {
+                    const float4 dd = sm.dd[x][warp][j][pr];
+                    float2 bc[NS];
+                    if constexpr (NS == 1) {
+                        bc[0] = f[j * NP];
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < NS; q += 2) {
+                            const float4 v = *reinterpret_cast<const float4 *>(f + j * NP + q);
+                            bc[q] = make_float2(v.x, v.y);
+                            bc[q + 1] = make_float2(v.z, v.w);
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < NS; ++q) {
+                        const float2 x = upk(fma2(pk(dd.x, dd.y), pk(A[q].x, A[q].y), pk(kDecayShift, kDecayShift)));
+                        h[q].x = fmaf(ex2f(x.x), h[q].x, dd.z * bc[q].x);
+                        h[q].y = fmaf(ex2f(x.y), h[q].y, dd.w * bc[q].x);
+                        if (!kStates) {
+                            acc[j].x = q == 0 ? h[q].x * bc[q].y : fmaf(h[q].x, bc[q].y, acc[j].x);
+                            acc[j].y = q == 0 ? h[q].y * bc[q].y : fmaf(h[q].y, bc[q].y, acc[j].y);
+                        }
+                    }
+                    sum.x += dd.x;
+                    sum.y += dd.y;
+                }
+                if (!kStates && j == 0) finish(1, out, before, x ^ 1, yp, before_valid);
+                if (TB <= 4) {
+                    if (j < 3) prepare(j + 1, next, w, r, x ^ 1);
+                } else if (j % (TB / 4) == 0 && j / (TB / 4) < 3) {
+                    prepare(j / (TB / 4) + 1, next, w, r, x ^ 1);
+                }
+            }
+            if (kStates) {
+                steps.x += sum.x;
+                steps.y += sum.y;
+            } else {
+#pragma unroll
+                for (int j = 0; j < TB; ++j) sm.yp[x][warp][j][lane] = acc[j];
+            }
+            before = now;
+            now = next;
+            before_valid = valid;
+            __syncwarp();
+        };
+        constexpr int NB = kTile / TB;     // blocks of a tile: an even number, so the exchange buffers alternate in step
+        static_assert(NB % 2 == 0, "parity");
+        for (int k = from; k < tiles; ++k) {
+            const int t0 = tile_begin(k), n = rows_of(k), buf1 = buf == 2 ? 0 : buf + 1;
+            cp_wait<0>();
+            cta_sync<THREADS>();  // tile k + 1 has landed, B and C of tile k are laid out, tile k - 1 is computed
+            if (k + 2 < tiles) stage(k + 2);
+            if (k + 1 < tiles) fetch_bc(k + 1);
+            const float2 *f = &sm.f[k & 1][0][n0];
+            const T *r0 = raw_row(buf), *r1 = raw_row(buf1);
+            if (n == kTile) {
+#pragma unroll
+                for (int q = 0; q < NB; ++q) {
+                    block(f + q * TB * NP, q + 1 < NB ? r0 + (q + 1) * TB * kCh : r1, q & 1, TB, Flag<true>{});
+                    yp += y_step;
+                }
+            } else {              // the first or the last tile of a request: blocks past its end change nothing
+                const int64_t skipped = (int64_t)(kTile - n) * s.ys;
+#pragma unroll 1
+                for (int q = 0; q < NB; ++q) {
+                    block(f + q * TB * NP, q + 1 < NB ? r0 + (q + 1) * TB * kCh : r1, q & 1, n - q * TB, Flag<false>{});
+                    yp += y_step;
+                }
+                if (!kStates) {
+                    float2 out[OWN];
+                    finish(0, out, before, 1, yp, before_valid);
+                    finish(1, out, before, 1, yp, before_valid);
+                }
+                before_valid = 0;
+                yp -= skipped;    // the next tile's rows follow the last that is there
+            }
+            buf = buf1;
+            if (k + 1 < tiles) widen_bc(k + 1);
+            if (!kStates && table) {
+                const int pos = done + t0 + n;
+                if (pos % s.block_size == 0) {
+                    const int col = pos / s.block_size - 1;
+                    if (col >= s.bt_width) {
+                        if (first) atomicOr(io.device_err, SSD_DEVERR_BLOCK_TABLE);
+                    } else {
+                        const int slot = io.block_table[(size_t)i * s.bt_width + col];
+                        if (slot >= s.num_slots) {
+                            if (first) atomicOr(io.device_err, SSD_DEVERR_BLOCK_SLOT);
+                        } else if (slot >= 0) {
+                            put(io.state_pool + (size_t)slot * dn);
+                        }
+                    }
+                }
+            }
+        }
+        if (!kStates) {
+            float2 out[OWN];
+            finish(0, out, before, 1, yp, before_valid);
+            finish(1, out, before, 1, yp, before_valid);
+        }
+    }
+    if (kStates) {
+        put(p.seg_state + (size_t)place * dn);
+        if (l == 0 && mine[0]) p.seg_steps[(size_t)place * s.D + d] = steps.x;
+        if (l == 0 && mine[1]) p.seg_steps[(size_t)place * s.D + d + 1] = steps.y;
+        return;
+    }
+    if (!ends) return;
+    if (io.final_states) put(io.final_states + (size_t)i * dn);
+    if (io.final_slots) {
+        const int slot = io.final_slots[i];
+        if (slot >= s.num_slots) {
+            if (first) atomicOr(io.device_err, SSD_DEVERR_FINAL_SLOT);
+        } else if (slot >= 0) {
+            put(io.state_pool + (size_t)slot * dn);
+        }
+    }
+}
+
+template <typename T, int NP, int L, bool kCommon, bool kStates>
+cudaError_t launch_g(const SelParams &p, cudaStream_t stream) {
+    constexpr auto kernel = selective_kernel<T, NP, L, kCommon, kStates>;
+    constexpr size_t smem = sizeof(typename Cfg<T, NP, L>::Smem);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t rows = p.seg ? seg_places(p.s.T, p.s.R, p.seg) : p.s.R;
+    return launch_after_prev(kernel, dim3((unsigned)(p.tiles * rows)), dim3(kPairs * L), smem, stream, p);
+}
+
+template <typename T, int NP, int L>
+cudaError_t launch_k(const SelParams &p, cudaStream_t stream) {
+    if (p.seg) {
+        const cudaError_t e = launch_g<T, NP, L, false, true>(p, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return p.s.softplus && p.io.z && p.y_pair ? launch_g<T, NP, L, true, false>(p, stream)
+                                              : launch_g<T, NP, L, false, false>(p, stream);
+}
+
+
+template <typename T>
+cudaError_t launch_selective_t(const SelParams &p, cudaStream_t stream) {
+    if (p.s.N <= 4) return launch_k<T, 4, 2>(p, stream);
+    if (p.s.N <= 8) return launch_k<T, 8, 2>(p, stream);
+    // Sixteen states: four lanes a pair of channels where the GPU is full or requests are split, eight where up to two CTAs
+    // an SM leave a request's latency in the open (three short prompts 7.3 -> 6.7 us; 8 x 2048 tokens 472 -> 580 us).
+    if (p.s.N <= 16 && !p.seg && (int64_t)p.tiles * p.s.R <= 2 * 152) return launch_k<T, 16, 8>(p, stream);
+    if (p.s.N <= 16) return launch_k<T, 16, 4>(p, stream);
+    if (p.s.N <= 32) return launch_k<T, 32, 8>(p, stream);
+    if (p.s.N <= 64) return launch_k<T, 64, 8>(p, stream);
+    if (p.s.N <= 128) return launch_k<T, 128, 8>(p, stream);
+    return launch_k<T, 256, 8>(p, stream);
+}
+
+}  // namespace ssd

@@ -1,0 +1,8 @@
+// ssd_selective_bf16.cu -- the selective scan's kernels for bf16 elements.
+#include "selective_scan.cuh"
+
+namespace ssd {
+
+cudaError_t launch_selective_bf16(const SelParams &p, cudaStream_t stream) { return launch_selective_t<__nv_bfloat16>(p, stream); }
+
+}  // namespace ssd

@@ -22,12 +22,6 @@
 namespace ssd {
 namespace {
 
-#ifndef STEP_MIN
-#define STEP_MIN 4
-#endif
-#ifndef STEP_RING
-#define STEP_RING 3
-#endif
 constexpr int kStepThreads = 128;
 constexpr int kMaxRb = 32;        // requests of a warp: their slots sit in its lanes
 
@@ -57,12 +51,12 @@ __device__ __forceinline__ float4 some(const T *p, int n) {
 // QL lanes a channel with 4 NV states each (quad v of a lane: states 4 (l + QL v) ..), CPG channels a lane group.
 // kExact: N = 4 QL NV, whole tiles of channels, everything on its boundary: no access is guarded, offsets are constants.
 template <typename T, int QL, int NV, bool kExact>
-__global__ void __launch_bounds__(kStepThreads, QL == 32 && NV == 2 ? 2 : STEP_MIN)
+__global__ void __launch_bounds__(kStepThreads, QL == 32 && NV == 2 ? 2 : 4)
     selective_step_kernel(const __grid_constant__ SelStepParams p) {
     constexpr int GR = 32 / QL;               // lane groups of a warp
     constexpr int CPG = QL < 4 ? QL : 4;      // channels of a group
     constexpr int CW = GR * CPG;              // channels of a warp
-    constexpr int kRing = NV == 1 ? STEP_RING : 2;  // requests whose states a lane holds or has on their way
+    constexpr int kRing = NV == 1 ? 3 : 2;  // requests whose states a lane holds or has on their way
     __shared__ float4 ring[kRing][CPG][NV][kStepThreads];
     pdl_wait();
     const SelShape &s = p.s;
