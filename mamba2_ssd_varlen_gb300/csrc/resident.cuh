@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 namespace ssd {
 
 constexpr int kResidentDevices = 64;
@@ -28,6 +30,13 @@ inline cudaError_t resident_ctas_at(int64_t (&cached)[kResidentDevices], void (*
     out = (int64_t)per_sm * sms;
     if (keep) cached[dev] = out;
     return cudaSuccess;
+}
+
+// How many items each worker takes one after the other, so that `items` of them make whole waves of at most `wave`
+// resident workers and none starts a nearly empty one; at most `most`.
+inline int64_t runs_of(int64_t items, int64_t wave, int64_t most) {
+    const int64_t waves = std::max<int64_t>(1, (items + wave * most - 1) / (wave * most));
+    return std::max<int64_t>(1, (items + wave * waves - 1) / (wave * waves));
 }
 
 }  // namespace ssd

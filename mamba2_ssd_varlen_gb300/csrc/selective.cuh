@@ -66,7 +66,7 @@ struct SelParams {
     const int32_t *cu;
     ssd_selective_io io;
     int32_t tiles;   // channel tiles of a request: G * ceil((D / G) / 32)
-    int32_t vec;     // u, delta, z: every tile row of a CTA starts on a 16-byte boundary
+    int32_t vec;     // u, delta, z: rows of a CTA's channels start on 16-byte (2), on 4-byte (1) or on other (0) boundaries
     int32_t bc_vec;  // B, C: every four states of a row start on a boundary of four elements
     int32_t y_pair;  // y: every pair of channels starts on a boundary of two elements
     int32_t ordered; // CTAs take the requests longest first

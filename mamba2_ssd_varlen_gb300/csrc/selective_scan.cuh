@@ -15,7 +15,7 @@
 //     and u, delta, z and y move as pairs) and NP / L of their states, L lanes a pair;
 //   - u, delta and z arrive by tiles of 16 tokens through asynchronous copies, two tiles
 //     ahead; B and C through registers, a tile ahead, laid out in shared memory as the
-//     (B, B, C, C) that a packed pair multiplies by: one 16-byte load a state;
+//     (B, C) that a state needs, two states a 16-byte load;
 //   - softplus, u dt', the skip term and the gate are computed by the L lanes of a pair
 //     for different tokens, and exchanged through shared memory.  They, and the sums over
 //     the L lanes, belong to the blocks of TB tokens after and before the one whose
@@ -28,12 +28,6 @@
 #include "special.cuh"
 
 namespace ssd {
-
-template <typename T>
-__device__ __forceinline__ void cp_elem(T *smem, const T *gmem) {
-    if constexpr (sizeof(T) == 4) cp4(smem, gmem);
-    else *smem = *gmem;  // two bytes: no asynchronous copy is that small
-}
 
 template <int THREADS>
 __device__ __forceinline__ void cta_sync() {
@@ -89,18 +83,12 @@ template <>
 struct Four<float> {
     float4 v;
     __device__ __forceinline__ void load(const float *p) { v = *reinterpret_cast<const float4 *>(p); }
-    __device__ __forceinline__ void set(int j, float x) { (&v.x)[j] = x; }
     __device__ __forceinline__ float4 get() const { return v; }
 };
 template <>
 struct Four<__nv_bfloat16> {
     uint2 v;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = *reinterpret_cast<const uint2 *>(p); }
-    __device__ __forceinline__ void set(int j, __nv_bfloat16 x) {
-        const uint32_t b = *reinterpret_cast<const unsigned short *>(&x);
-        uint32_t &w = j < 2 ? v.x : v.y;
-        w = j & 1 ? (w & 0xFFFFu) | b << 16 : (w & 0xFFFF0000u) | b;
-    }
     __device__ __forceinline__ float4 get() const {
         return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
                            __uint_as_float(v.y & 0xFFFF0000u));
@@ -154,7 +142,8 @@ __device__ __forceinline__ int seg_request(const SelParams &p, int place) {
     return lo;
 }
 
-// kCommon: softplus, a gate, and pairs of y on their boundaries (what a layer has); else these are looked up.
+// kCommon: softplus, a gate, and rows on the boundaries of their copies and stores (what a layer has); else all that is
+// looked up.
 // kStates: only the states that segments leave behind, from zeros; no outputs.
 template <typename T, int NP, int L, bool kCommon, bool kStates>
 __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kernel(const __grid_constant__ SelParams p) {
@@ -226,7 +215,7 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
     const T *sz = gz + (tile_begin(from) + sr) * s.zs + sc;
     auto stage = [&](int k) {
         const int n = rows_of(k), st = k % 3;
-        if (p.vec) {
+        if (p.vec == 2) {
 #pragma unroll
             for (int m = 0; m < PASSES; ++m) {
                 const int r = sr + m * ROWS;
@@ -237,14 +226,15 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
                     if (!kStates && (kCommon || gz)) cp16(dst + 2 * kTile * kCh, sz + m * ROWS * s.zs);
                 }
             }
-        } else {
-            for (int q = tid; q < n * kCh; q += THREADS) {
-                const int r = q / kCh, col = q % kCh;
+        } else if (p.vec == 1) {
+            constexpr int EW = 4 / sizeof(T), W = kCh / EW;  // elements of a word, words of a row
+            for (int q = tid; q < n * W; q += THREADS) {
+                const int r = q / W, col = q % W * EW;
                 if (col >= width) continue;
                 T *dst = &sm.raw[st][0][r][col ^ swizzle<T>(r)];
-                cp_elem(dst, su + (int64_t)(r - sr) * s.us + (col - sc));
-                cp_elem(dst + kTile * kCh, sd + (int64_t)(r - sr) * s.ds + (col - sc));
-                if (!kStates && (kCommon || gz)) cp_elem(dst + 2 * kTile * kCh, sz + (int64_t)(r - sr) * s.zs + (col - sc));
+                cp4(dst, su + (int64_t)(r - sr) * s.us + (col - sc));
+                cp4(dst + kTile * kCh, sd + (int64_t)(r - sr) * s.ds + (col - sc));
+                if (!kStates && (kCommon || gz)) cp4(dst + 2 * kTile * kCh, sz + (int64_t)(r - sr) * s.zs + (col - sc));
             }
         }
         su += n * s.us;
@@ -252,25 +242,56 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
         sz += n * s.zs;
         cp_commit();
     };
+    // Two-byte rows off four-byte boundaries, which no asynchronous copy takes: through registers, a tile's walk ahead.
+    constexpr bool kElements = sizeof(T) == 2 && !kCommon;
+    constexpr int EP = kElements ? kTile * kCh / THREADS : 1;
+    T eu[EP], ed[EP], ez[EP];
+    auto fetch_elements = [&](int k) {
+        if (!kElements || p.vec != 0) return;
+        const int64_t t0 = tile_begin(k);
+        const int n = rows_of(k);
+#pragma unroll
+        for (int m = 0; m < EP; ++m) {
+            const int r = (tid + m * THREADS) / kCh, col = (tid + m * THREADS) % kCh;
+            if (r < n && col < width) {
+                eu[m] = gu[(t0 + r) * s.us + col];
+                ed[m] = gd[(t0 + r) * s.ds + col];
+                if (gz) ez[m] = gz[(t0 + r) * s.zs + col];
+            }
+        }
+    };
+    auto put_elements = [&](int k) {
+        if (!kElements || p.vec != 0) return;
+#pragma unroll
+        for (int m = 0; m < EP; ++m) {
+            const int r = (tid + m * THREADS) / kCh, col = (tid + m * THREADS) % kCh;
+            T *dst = &sm.raw[k % 3][0][r][col ^ swizzle<T>(r)];
+            dst[0] = eu[m];
+            dst[kTile * kCh] = ed[m];
+            if (gz) dst[2 * kTile * kCh] = ez[m];
+        }
+    };
     Four<T> bq[IT], cq[IT];            // B and C of the next tile on their way
+    T be[kCommon ? 1 : IT][4], ce[kCommon ? 1 : IT][4];  // the same where they come one element a load
     auto fetch_bc = [&](int k) {
         const int t0 = tile_begin(k), n = rows_of(k);
 #pragma unroll
         for (int q = 0; q < IT; ++q) {
             const int e = tid + q * THREADS, r = e / (NP / 4), n4 = e % (NP / 4) * 4;
-            bq[q] = {}, cq[q] = {};
-            if (e >= K::QUADS || r >= n || n4 >= s.N) continue;
+            const bool there = e < K::QUADS && r < n;
             const T *sb = gb + (size_t)(t0 + r) * s.bs + n4, *sc = gc + (size_t)(t0 + r) * s.cs + n4;
-            if (p.bc_vec) {
-                bq[q].load(sb);
-                cq[q].load(sc);
+            if (kCommon || p.bc_vec) {
+                bq[q] = {}, cq[q] = {};
+                if (there && n4 < s.N) {
+                    bq[q].load(sb);
+                    cq[q].load(sc);
+                }
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (n4 + j < s.N) {
-                        bq[q].set(j, sb[j]);
-                        cq[q].set(j, sc[j]);
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    be[kCommon ? 0 : q][j] = there && n4 + j < s.N ? sb[j] : from_f32<T>(0.f);
+                    ce[kCommon ? 0 : q][j] = there && n4 + j < s.N ? sc[j] : from_f32<T>(0.f);
+                }
             }
         }
     };
@@ -279,7 +300,14 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
         for (int q = 0; q < IT; ++q) {
             const int e = tid + q * THREADS, r = e / (NP / 4), n4 = e % (NP / 4) * 4;
             if (e >= K::QUADS) continue;
-            const float4 bv = bq[q].get(), cv = cq[q].get();
+            float4 bv, cv;
+            if (kCommon || p.bc_vec) {
+                bv = bq[q].get(), cv = cq[q].get();
+            } else {
+                const T *x = be[kCommon ? 0 : q], *w = ce[kCommon ? 0 : q];
+                bv = make_float4(to_f32(x[0]), to_f32(x[1]), to_f32(x[2]), to_f32(x[3]));
+                cv = make_float4(to_f32(w[0]), to_f32(w[1]), to_f32(w[2]), to_f32(w[3]));
+            }
             float4 *dst = reinterpret_cast<float4 *>(&sm.f[k & 1][r][n4]);
             dst[0] = make_float4(bv.x, cv.x, bv.y, cv.y);
             dst[1] = make_float4(bv.z, cv.z, bv.w, cv.w);
@@ -288,7 +316,13 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
 
     if (tiles > from && len > 0) {  // the first copies: what follows up to the first tile runs beside them
         stage(from);
-        if (tiles > from + 1) stage(from + 1);
+        fetch_elements(from);
+        put_elements(from);
+        if (tiles > from + 1) {
+            stage(from + 1);
+            fetch_elements(from + 1);
+            put_elements(from + 1);
+        }
         fetch_bc(from);
     }
 
@@ -498,7 +532,10 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
             const int t0 = tile_begin(k), n = rows_of(k), buf1 = buf == 2 ? 0 : buf + 1;
             cp_wait<0>();
             cta_sync<THREADS>();  // tile k + 1 has landed, B and C of tile k are laid out, tile k - 1 is computed
-            if (k + 2 < tiles) stage(k + 2);
+            if (k + 2 < tiles) {
+                stage(k + 2);
+                fetch_elements(k + 2);
+            }
             if (k + 1 < tiles) fetch_bc(k + 1);
             const float2 *f = &sm.f[k & 1][0][n0];
             const T *r0 = raw_row(buf), *r1 = raw_row(buf1);
@@ -525,6 +562,7 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
             }
             buf = buf1;
             if (k + 1 < tiles) widen_bc(k + 1);
+            if (k + 2 < tiles) put_elements(k + 2);
             if (!kStates && table) {
                 const int pos = done + t0 + n;
                 if (pos % s.block_size == 0) {
@@ -584,7 +622,7 @@ cudaError_t launch_k(const SelParams &p, cudaStream_t stream) {
         const cudaError_t e = launch_g<T, NP, L, false, true>(p, stream);
         if (e != cudaSuccess) return e;
     }
-    return p.s.softplus && p.io.z && p.y_pair ? launch_g<T, NP, L, true, false>(p, stream)
+    return p.s.softplus && p.io.z && p.y_pair && p.bc_vec && p.vec ? launch_g<T, NP, L, true, false>(p, stream)
                                               : launch_g<T, NP, L, false, false>(p, stream);
 }
 

@@ -159,8 +159,7 @@ cudaError_t launch_cs_n(ConvStepParams &p, cudaStream_t stream) {
     const cudaError_t e = resident_ctas_at(cached, kernel, kCsThreads, 0, resident);
     if (e != cudaSuccess) return e;
     p.tiles = (p.D + kCsThreads * kN - 1) / (kCsThreads * kN);
-    // requests a CTA, one after the other with the weights in registers: as many as leave one wave of resident CTAs
-    p.rb = (int)std::min<int64_t>(32, std::max<int64_t>(1, ((int64_t)p.tiles * p.R + resident - 1) / resident));
+    p.rb = (int)runs_of((int64_t)p.tiles * p.R, resident, 32);  // requests a CTA, with the weights in registers
     const int64_t ctas = (int64_t)p.tiles * ((p.R + p.rb - 1) / p.rb);
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     return launch_after_prev(kernel, dim3((unsigned)ctas), dim3(kCsThreads), 0, stream, p);

@@ -70,13 +70,13 @@ extern "C" int ssd_varlen_selective_scan(const ssd_selective_dims *d, const int3
     p.cu = cu_seqlens;
     p.io = *io;
     p.tiles = (int32_t)tiles;
-    auto rows16 = [&](const void *ptr, int64_t stride, int64_t step) {  // rows and their parts on 16-byte boundaries
-        return sel_aligned(ptr, 16) && stride * e % 16 == 0 && step * e % 16 == 0;
-    };
-    p.vec = rows16(io->u, p.s.us, dg) && rows16(io->delta, p.s.ds, dg) && (!io->z || rows16(io->z, p.s.zs, dg));
     auto rows = [&](const void *ptr, int64_t stride, int64_t step, int64_t n) {  // on boundaries of n elements
         return sel_aligned(ptr, n * e) && stride % n == 0 && step % n == 0;
     };
+    auto all = [&](int64_t n) {
+        return rows(io->u, p.s.us, dg, n) && rows(io->delta, p.s.ds, dg, n) && (!io->z || rows(io->z, p.s.zs, dg, n));
+    };
+    p.vec = all(16 / e) ? 2 : all(4 / e) ? 1 : 0;
     p.bc_vec = rows(io->B, p.s.bs, d->N, 4) && rows(io->C, p.s.cs, d->N, 4);
     p.y_pair = rows(io->y, p.s.ys, dg, 2);
     const cudaError_t err = d->dtype == SSD_DTYPE_BF16 ? launch_selective_bf16(p, stream) : launch_selective_f32(p, stream);

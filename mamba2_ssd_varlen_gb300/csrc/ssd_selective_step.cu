@@ -284,9 +284,8 @@ cudaError_t launch_step_e(SelStepParams &p, cudaStream_t stream) {
     int64_t resident = 0;
     const cudaError_t e = resident_ctas_at(cached, kernel, kStepThreads, 0, resident);
     if (e != cudaSuccess) return e;
-    // requests a warp: as many as leave one wave of resident warps, so that none waits for a second
-    const int64_t tiles = (int64_t)((p.s.D / p.s.G + CW - 1) / CW) * p.s.G, wave = resident * kWarps;
-    p.rb = (int)std::min<int64_t>(kMaxRb, std::max<int64_t>(1, (tiles * p.s.R + wave - 1) / wave));
+    const int64_t tiles = (int64_t)((p.s.D / p.s.G + CW - 1) / CW) * p.s.G;
+    p.rb = (int)runs_of(tiles * p.s.R, resident * kWarps, kMaxRb);
     const int64_t items = tiles * ((p.s.R + p.rb - 1) / p.rb);
     if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     return launch_after_prev(kernel, dim3((unsigned)((items + kWarps - 1) / kWarps)), dim3(kStepThreads), 0, stream, p);

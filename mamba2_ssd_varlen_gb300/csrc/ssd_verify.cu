@@ -25,6 +25,9 @@ namespace cg = cooperative_groups;
 namespace ssd {
 namespace {
 
+#ifndef VMIN
+#define VMIN 4
+#endif
 constexpr int kVerThreads = 256;
 constexpr int kChunk = 1024;     // vocabulary entries of a warp's chunk
 constexpr int kMaxCluster = 8;   // the portable limit
@@ -40,8 +43,7 @@ struct VerifyParams {
 // whose bias is taken off at the end (arithmetic modulo 2^32: up to 2^12 terms).
 struct Digits {
     uint32_t hi = 0, lo = 0;
-    __device__ __forceinline__ void add(float w) {
-        w = fminf(fmaxf(w, 0.f), 1.f);  // a NaN counts as 0
+    __device__ __forceinline__ void add(float w) {  // w in [0, 1]
         const float t = __fmaf_rz(w, 1048576.f, 8388608.f);
         const float rem = fmaf(w, 1048576.f, 8388608.f - t);  // exact
         const float u = __fmaf_rz(rem, 1048576.f, 8388608.f);
@@ -110,20 +112,21 @@ __device__ __forceinline__ void load_part(const Row<T> &row, int c, int e0, int 
         }
     };
     fetch(row.p, w);
+    // clamped to [0, 1], 0 for a NaN: the subtraction's saturation
     if (row.q) {
         float q[kE][kVec];
         fetch(row.q, q);
 #pragma unroll
         for (int e = 0; e < kE; ++e)
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) w[e][j] -= q[e][j];
-    }
-    if ((unsigned)(row.drafted - c * kChunk) < (unsigned)kChunk) {
+            for (int j = 0; j < kVec; ++j) w[e][j] = __saturatef(w[e][j] - q[e][j]);
+    } else {
+        const bool here = (unsigned)(row.drafted - c * kChunk) < (unsigned)kChunk;
 #pragma unroll
         for (int e = 0; e < kE; ++e)
 #pragma unroll
             for (int j = 0; j < kVec; ++j)
-                if (v0 + e * 32 * kVec + j == row.drafted) w[e][j] -= 1.f;
+                w[e][j] = __saturatef(here && v0 + e * 32 * kVec + j == row.drafted ? w[e][j] - 1.f : w[e][j]);
     }
 }
 
@@ -132,7 +135,7 @@ __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 template <typename T, int kVec>
-__global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_constant__ VerifyParams p) {
+__global__ void __launch_bounds__(kVerThreads, kVec == 1 ? VMIN - 1 : VMIN) verify_kernel(const __grid_constant__ VerifyParams p) {
     constexpr int kWarps = kVerThreads / 32, kLoads = kChunk / (32 * kVec);
     constexpr int kBatch = kVec == 1 ? 16 : 4;  // loads of a row in flight a lane
     extern __shared__ unsigned long long chunk_sum[];  // of this CTA's chunks
