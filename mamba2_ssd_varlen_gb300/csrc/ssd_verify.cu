@@ -25,9 +25,6 @@ namespace cg = cooperative_groups;
 namespace ssd {
 namespace {
 
-#ifndef VMIN
-#define VMIN 4
-#endif
 constexpr int kVerThreads = 256;
 constexpr int kChunk = 1024;     // vocabulary entries of a warp's chunk
 constexpr int kMaxCluster = 8;   // the portable limit
@@ -121,12 +118,17 @@ __device__ __forceinline__ void load_part(const Row<T> &row, int c, int e0, int 
 #pragma unroll
             for (int j = 0; j < kVec; ++j) w[e][j] = __saturatef(w[e][j] - q[e][j]);
     } else {
-        const bool here = (unsigned)(row.drafted - c * kChunk) < (unsigned)kChunk;
+        if ((unsigned)(row.drafted - c * kChunk) < (unsigned)kChunk) {
+#pragma unroll
+            for (int e = 0; e < kE; ++e)
+#pragma unroll
+                for (int j = 0; j < kVec; ++j)
+                    if (v0 + e * 32 * kVec + j == row.drafted) w[e][j] -= 1.f;
+        }
 #pragma unroll
         for (int e = 0; e < kE; ++e)
 #pragma unroll
-            for (int j = 0; j < kVec; ++j)
-                w[e][j] = __saturatef(here && v0 + e * 32 * kVec + j == row.drafted ? w[e][j] - 1.f : w[e][j]);
+            for (int j = 0; j < kVec; ++j) w[e][j] = __saturatef(w[e][j]);
     }
 }
 
@@ -135,7 +137,7 @@ __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 template <typename T, int kVec>
-__global__ void __launch_bounds__(kVerThreads, kVec == 1 ? VMIN - 1 : VMIN) verify_kernel(const __grid_constant__ VerifyParams p) {
+__global__ void __launch_bounds__(kVerThreads, kVec == 1 ? 3 : 4) verify_kernel(const __grid_constant__ VerifyParams p) {
     constexpr int kWarps = kVerThreads / 32, kLoads = kChunk / (32 * kVec);
     constexpr int kBatch = kVec == 1 ? 16 : 4;  // loads of a row in flight a lane
     extern __shared__ unsigned long long chunk_sum[];  // of this CTA's chunks
@@ -306,10 +308,10 @@ __global__ void __launch_bounds__(kVerThreads, kVec == 1 ? VMIN - 1 : VMIN) veri
 template <typename T, int kVec>
 cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream) {
     const int chunks = (p.V + kChunk - 1) / kChunk;
-    // CTAs a window: enough for four on every SM, but at least a chunk for each of a CTA's warps, so that few
-    // windows spread over the GPU and many do not pay for a cluster's barriers.
+    // CTAs a window: as many as the GPU holds at once (four an SM), but at least a chunk for each of a CTA's warps, so
+    // that few windows spread over the GPU and many do not pay for a cluster's barriers or a second wave.
     int S = 1;
-    while (S < kMaxCluster && (int64_t)p.R * S < 4 * 152 && chunks >= 2 * S * (kVerThreads / 32)) S *= 2;
+    while (S < kMaxCluster && (int64_t)p.R * S * 2 <= 4 * 152 && chunks >= 2 * S * (kVerThreads / 32)) S *= 2;
     const size_t smem = (size_t)((chunks + S - 1) / S + 1) * sizeof(unsigned long long);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
