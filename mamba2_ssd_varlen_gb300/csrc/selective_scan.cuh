@@ -56,6 +56,10 @@ template <bool v>
 struct Flag {
     static constexpr bool value = v;
 };
+template <int v>
+struct Count {
+    static constexpr int value = v;
+};
 
 // Two neighbouring elements to and from fp32.
 __device__ __forceinline__ float2 load_pair(const float *p) { return *reinterpret_cast<const float2 *>(p); }
@@ -73,6 +77,17 @@ __device__ __forceinline__ void store_pair_if(bool on, __nv_bfloat16 *p, float2 
     const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
     asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %0, 0;\n @q st.global.b32 [%1], %2;\n}" ::"r"((int)on), "l"(p),
                  "r"(*reinterpret_cast<const uint32_t *>(&b))
+                 : "memory");
+}
+
+__device__ __forceinline__ void store_if(bool on, float *p, float v) {
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %0, 0;\n @q st.global.f32 [%1], %2;\n}" ::"r"((int)on), "l"(p), "f"(v)
+                 : "memory");
+}
+__device__ __forceinline__ void store_if(bool on, __nv_bfloat16 *p, float v) {
+    const __nv_bfloat16 b = __float2bfloat16_rn(v);
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %0, 0;\n @q st.global.b16 [%1], %2;\n}" ::"r"((int)on), "l"(p),
+                 "h"(*reinterpret_cast<const unsigned short *>(&b))
                  : "memory");
 }
 
@@ -142,10 +157,10 @@ __device__ __forceinline__ int seg_request(const SelParams &p, int place) {
     return lo;
 }
 
-// kCommon: softplus, a gate, and rows on the boundaries of their copies and stores (what a layer has); else all that is
-// looked up.
+// kLayer: softplus and a gate (what a layer has); else they are looked up.  kRows: rows on the boundaries of their copies
+// and stores; else they are looked up too, and rows may come element by element.
 // kStates: only the states that segments leave behind, from zeros; no outputs.
-template <typename T, int NP, int L, bool kCommon, bool kStates>
+template <typename T, int NP, int L, bool kLayer, bool kRows, bool kStates>
 __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kernel(const __grid_constant__ SelParams p) {
     using K = Cfg<T, NP, L>;
     constexpr int NS = K::NS, PW = K::PW, OWN = K::OWN, TB = K::TB, THREADS = K::THREADS, IT = K::IT;
@@ -194,7 +209,7 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
     }
 
     const T *gu = static_cast<const T *>(io.u) + a * s.us + d0, *gd = static_cast<const T *>(io.delta) + a * s.ds + d0;
-    const T *gz = !kStates && (kCommon || io.z) ? static_cast<const T *>(io.z) + a * s.zs + d0 : nullptr;
+    const T *gz = !kStates && (kLayer || io.z) ? static_cast<const T *>(io.z) + a * s.zs + d0 : nullptr;
     const T *gb = static_cast<const T *>(io.B) + a * s.bs + (size_t)g * s.N;
     const T *gc = static_cast<const T *>(io.C) + a * s.cs + (size_t)g * s.N;
     T *gy = static_cast<T *>(io.y) + a * s.ys + d;
@@ -207,72 +222,65 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
     if ((part > 0 && from >= all) || (kStates && ends)) return;  // no such segment; nobody needs its state
     auto tile_begin = [&](int k) { return k == 0 ? 0 : k * kTile - lead; };
     auto rows_of = [&](int k) { return min(len, (k + 1) * kTile - lead) - tile_begin(k); };
-    // Asynchronous copies of u, delta and z of tile k; called for one tile after the other.
-    constexpr int E = 16 / sizeof(T), V = kCh / E;                  // elements of a vector, vectors of a row
-    constexpr int ROWS = THREADS / V, PASSES = (kTile + ROWS - 1) / ROWS;
-    const int sr = tid / V, sc = tid % V * E;                       // this thread's first row and column of a tile
+    // Copies of u, delta and z of tile k, asked for one tile after the other: asynchronous ones by vectors or by words, or
+    // -- two-byte rows off four-byte boundaries, which no asynchronous copy takes -- through registers, put in their places
+    // (put_elements) a tile's walk later.  A thread keeps to one column, and its rows are ROWS apart.
+    constexpr bool kElements = sizeof(T) == 2 && !kRows;
+    constexpr int EP = kElements ? kTile * kCh / THREADS : 1;
+    const int unit = p.vec == 2 ? 16 / (int)sizeof(T) : p.vec == 1 ? 4 / (int)sizeof(T) : 1;  // elements of a copy
+    const int sr = tid / (kCh / unit), sc = tid % (kCh / unit) * unit;  // the thread's first row and column of a tile
     const T *su = gu + (tile_begin(from) + sr) * s.us + sc, *sd = gd + (tile_begin(from) + sr) * s.ds + sc;
     const T *sz = gz + (tile_begin(from) + sr) * s.zs + sc;
+    T eu[EP], ed[EP], ez[EP];
     auto stage = [&](int k) {
         const int n = rows_of(k), st = k % 3;
-        if (p.vec == 2) {
+        auto copies = [&](auto elements, auto copy) {
+            constexpr int ROWS = THREADS / (kCh / elements.value), PASSES = (kTile + ROWS - 1) / ROWS;
 #pragma unroll
             for (int m = 0; m < PASSES; ++m) {
                 const int r = sr + m * ROWS;
-                if (r < n && sc < width) {
-                    T *dst = &sm.raw[st][0][r][sc ^ swizzle<T>(r)];
-                    cp16(dst, su + m * ROWS * s.us);
-                    cp16(dst + kTile * kCh, sd + m * ROWS * s.ds);
-                    if (!kStates && (kCommon || gz)) cp16(dst + 2 * kTile * kCh, sz + m * ROWS * s.zs);
-                }
+                if (r < n && sc < width) copy(m, &sm.raw[st][0][r][sc ^ swizzle<T>(r)], m * ROWS);
             }
+        };
+        if (p.vec == 2) {
+            copies(Count<16 / sizeof(T)>{}, [&](int, T *dst, int r) {
+                cp16(dst, su + r * s.us);
+                cp16(dst + kTile * kCh, sd + r * s.ds);
+                if (!kStates && (kLayer || gz)) cp16(dst + 2 * kTile * kCh, sz + r * s.zs);
+            });
         } else if (p.vec == 1) {
-            constexpr int EW = 4 / sizeof(T), W = kCh / EW;  // elements of a word, words of a row
-            for (int q = tid; q < n * W; q += THREADS) {
-                const int r = q / W, col = q % W * EW;
-                if (col >= width) continue;
-                T *dst = &sm.raw[st][0][r][col ^ swizzle<T>(r)];
-                cp4(dst, su + (int64_t)(r - sr) * s.us + (col - sc));
-                cp4(dst + kTile * kCh, sd + (int64_t)(r - sr) * s.ds + (col - sc));
-                if (!kStates && (kCommon || gz)) cp4(dst + 2 * kTile * kCh, sz + (int64_t)(r - sr) * s.zs + (col - sc));
-            }
+            copies(Count<4 / sizeof(T)>{}, [&](int, T *dst, int r) {
+                cp4(dst, su + r * s.us);
+                cp4(dst + kTile * kCh, sd + r * s.ds);
+                if (!kStates && (kLayer || gz)) cp4(dst + 2 * kTile * kCh, sz + r * s.zs);
+            });
+        } else if constexpr (kElements) {
+            copies(Count<1>{}, [&](int m, T *, int r) {
+                eu[m] = su[r * s.us];
+                ed[m] = sd[r * s.ds];
+                if (!kStates && (kLayer || gz)) ez[m] = sz[r * s.zs];
+            });
         }
         su += n * s.us;
         sd += n * s.ds;
         sz += n * s.zs;
         cp_commit();
     };
-    // Two-byte rows off four-byte boundaries, which no asynchronous copy takes: through registers, a tile's walk ahead.
-    constexpr bool kElements = sizeof(T) == 2 && !kCommon;
-    constexpr int EP = kElements ? kTile * kCh / THREADS : 1;
-    T eu[EP], ed[EP], ez[EP];
-    auto fetch_elements = [&](int k) {
-        if (!kElements || p.vec != 0) return;
-        const int64_t t0 = tile_begin(k);
-        const int n = rows_of(k);
+    auto put_elements = [&](int k) {
+        if constexpr (kElements) {
+            if (p.vec != 0) return;
 #pragma unroll
-        for (int m = 0; m < EP; ++m) {
-            const int r = (tid + m * THREADS) / kCh, col = (tid + m * THREADS) % kCh;
-            if (r < n && col < width) {
-                eu[m] = gu[(t0 + r) * s.us + col];
-                ed[m] = gd[(t0 + r) * s.ds + col];
-                if (gz) ez[m] = gz[(t0 + r) * s.zs + col];
+            for (int m = 0; m < EP; ++m) {
+                const int r = sr + m * (THREADS / kCh);
+                T *dst = &sm.raw[k % 3][0][r][sc ^ swizzle<T>(r)];
+                dst[0] = eu[m];
+                dst[kTile * kCh] = ed[m];
+                if (!kStates && (kLayer || gz)) dst[2 * kTile * kCh] = ez[m];
             }
         }
     };
-    auto put_elements = [&](int k) {
-        if (!kElements || p.vec != 0) return;
-#pragma unroll
-        for (int m = 0; m < EP; ++m) {
-            const int r = (tid + m * THREADS) / kCh, col = (tid + m * THREADS) % kCh;
-            T *dst = &sm.raw[k % 3][0][r][col ^ swizzle<T>(r)];
-            dst[0] = eu[m];
-            dst[kTile * kCh] = ed[m];
-            if (gz) dst[2 * kTile * kCh] = ez[m];
-        }
-    };
     Four<T> bq[IT], cq[IT];            // B and C of the next tile on their way
-    T be[kCommon ? 1 : IT][4], ce[kCommon ? 1 : IT][4];  // the same where they come one element a load
+    T be[kRows ? 1 : IT][4], ce[kRows ? 1 : IT][4];  // the same where they come one element a load
     auto fetch_bc = [&](int k) {
         const int t0 = tile_begin(k), n = rows_of(k);
 #pragma unroll
@@ -280,7 +288,7 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
             const int e = tid + q * THREADS, r = e / (NP / 4), n4 = e % (NP / 4) * 4;
             const bool there = e < K::QUADS && r < n;
             const T *sb = gb + (size_t)(t0 + r) * s.bs + n4, *sc = gc + (size_t)(t0 + r) * s.cs + n4;
-            if (kCommon || p.bc_vec) {
+            if (kRows || p.bc_vec) {
                 bq[q] = {}, cq[q] = {};
                 if (there && n4 < s.N) {
                     bq[q].load(sb);
@@ -289,8 +297,8 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    be[kCommon ? 0 : q][j] = there && n4 + j < s.N ? sb[j] : from_f32<T>(0.f);
-                    ce[kCommon ? 0 : q][j] = there && n4 + j < s.N ? sc[j] : from_f32<T>(0.f);
+                    be[kRows ? 0 : q][j] = there && n4 + j < s.N ? sb[j] : from_f32<T>(0.f);
+                    ce[kRows ? 0 : q][j] = there && n4 + j < s.N ? sc[j] : from_f32<T>(0.f);
                 }
             }
         }
@@ -301,10 +309,10 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
             const int e = tid + q * THREADS, r = e / (NP / 4), n4 = e % (NP / 4) * 4;
             if (e >= K::QUADS) continue;
             float4 bv, cv;
-            if (kCommon || p.bc_vec) {
+            if (kRows || p.bc_vec) {
                 bv = bq[q].get(), cv = cq[q].get();
             } else {
-                const T *x = be[kCommon ? 0 : q], *w = ce[kCommon ? 0 : q];
+                const T *x = be[kRows ? 0 : q], *w = ce[kRows ? 0 : q];
                 bv = make_float4(to_f32(x[0]), to_f32(x[1]), to_f32(x[2]), to_f32(x[3]));
                 cv = make_float4(to_f32(w[0]), to_f32(w[1]), to_f32(w[2]), to_f32(w[3]));
             }
@@ -316,11 +324,9 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
 
     if (tiles > from && len > 0) {  // the first copies: what follows up to the first tile runs beside them
         stage(from);
-        fetch_elements(from);
         put_elements(from);
         if (tiles > from + 1) {
             stage(from + 1);
-            fetch_elements(from + 1);
             put_elements(from + 1);
         }
         fetch_bc(from);
@@ -386,7 +392,7 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
     struct Steps {
         float2 v[OWN], e[OWN], r[OWN], z[OWN], ze[OWN];
     };
-    const bool softplus = kCommon || s.softplus, gated = !kStates && (kCommon || gz != nullptr);
+    const bool softplus = kLayer || s.softplus, gated = !kStates && (kLayer || gz != nullptr);
     // Four stages, each taking up what the special-function unit gave the one before it.
     auto prepare = [&](int stage, Own &o, Steps &w, const T *r, int x) {
 #pragma unroll
@@ -443,11 +449,11 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
                     v.y *= o.gate[q].y;
                 }
                 T *at = dst + (size_t)q * s.ys;
-                if (kCommon || p.y_pair) {
+                if (kRows || p.y_pair) {
                     store_pair_if(j < valid && mine[1], at, v);
                 } else {
-                    if (j < valid && mine[0]) at[0] = from_f32<T>(v.x);
-                    if (j < valid && mine[1]) at[1] = from_f32<T>(v.y);
+                    store_if(j < valid && mine[0], at, v.x);
+                    store_if(j < valid && mine[1], at + 1, v.y);
                 }
             }
         }
@@ -532,10 +538,7 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
             const int t0 = tile_begin(k), n = rows_of(k), buf1 = buf == 2 ? 0 : buf + 1;
             cp_wait<0>();
             cta_sync<THREADS>();  // tile k + 1 has landed, B and C of tile k are laid out, tile k - 1 is computed
-            if (k + 2 < tiles) {
-                stage(k + 2);
-                fetch_elements(k + 2);
-            }
+            if (k + 2 < tiles) stage(k + 2);
             if (k + 1 < tiles) fetch_bc(k + 1);
             const float2 *f = &sm.f[k & 1][0][n0];
             const T *r0 = raw_row(buf), *r1 = raw_row(buf1);
@@ -604,9 +607,9 @@ __global__ void __launch_bounds__(kPairs * L, Cfg<T, NP, L>::MIN) selective_kern
     }
 }
 
-template <typename T, int NP, int L, bool kCommon, bool kStates>
+template <typename T, int NP, int L, bool kLayer, bool kRows, bool kStates>
 cudaError_t launch_g(const SelParams &p, cudaStream_t stream) {
-    constexpr auto kernel = selective_kernel<T, NP, L, kCommon, kStates>;
+    constexpr auto kernel = selective_kernel<T, NP, L, kLayer, kRows, kStates>;
     constexpr size_t smem = sizeof(typename Cfg<T, NP, L>::Smem);
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -616,29 +619,31 @@ cudaError_t launch_g(const SelParams &p, cudaStream_t stream) {
     return launch_after_prev(kernel, dim3((unsigned)(p.tiles * rows)), dim3(kPairs * L), smem, stream, p);
 }
 
-template <typename T, int NP, int L>
+// kSpecial: instances for what a layer has beside the one for anything (few of the larger state sizes are met in layers).
+template <typename T, int NP, int L, bool kSpecial>
 cudaError_t launch_k(const SelParams &p, cudaStream_t stream) {
+    const bool layer = p.s.softplus && p.io.z, rows = p.y_pair && p.bc_vec && p.vec;
     if (p.seg) {
-        const cudaError_t e = launch_g<T, NP, L, false, true>(p, stream);
+        const cudaError_t e = kSpecial && layer && rows ? launch_g<T, NP, L, kSpecial, kSpecial, true>(p, stream)
+                                                        : launch_g<T, NP, L, false, false, true>(p, stream);
         if (e != cudaSuccess) return e;
     }
-    return p.s.softplus && p.io.z && p.y_pair && p.bc_vec && p.vec ? launch_g<T, NP, L, true, false>(p, stream)
-                                              : launch_g<T, NP, L, false, false>(p, stream);
+    if (kSpecial && layer && rows) return launch_g<T, NP, L, kSpecial, kSpecial, false>(p, stream);
+    if (kSpecial && layer) return launch_g<T, NP, L, kSpecial, false, false>(p, stream);
+    return launch_g<T, NP, L, false, false, false>(p, stream);
 }
-
 
 template <typename T>
 cudaError_t launch_selective_t(const SelParams &p, cudaStream_t stream) {
-    if (p.s.N <= 4) return launch_k<T, 4, 2>(p, stream);
-    if (p.s.N <= 8) return launch_k<T, 8, 2>(p, stream);
+    if (p.s.N <= 8) return launch_k<T, 8, 4, true>(p, stream);
     // Sixteen states: four lanes a pair of channels where the GPU is full or requests are split, eight where up to two CTAs
     // an SM leave a request's latency in the open (three short prompts 7.3 -> 6.7 us; 8 x 2048 tokens 472 -> 580 us).
-    if (p.s.N <= 16 && !p.seg && (int64_t)p.tiles * p.s.R <= 2 * 152) return launch_k<T, 16, 8>(p, stream);
-    if (p.s.N <= 16) return launch_k<T, 16, 4>(p, stream);
-    if (p.s.N <= 32) return launch_k<T, 32, 8>(p, stream);
-    if (p.s.N <= 64) return launch_k<T, 64, 8>(p, stream);
-    if (p.s.N <= 128) return launch_k<T, 128, 8>(p, stream);
-    return launch_k<T, 256, 8>(p, stream);
+    if (p.s.N <= 16 && !p.seg && (int64_t)p.tiles * p.s.R <= 2 * 152) return launch_k<T, 16, 8, true>(p, stream);
+    if (p.s.N <= 16) return launch_k<T, 16, 4, true>(p, stream);
+    if (p.s.N <= 32) return launch_k<T, 32, 8, true>(p, stream);
+    if (p.s.N <= 64) return launch_k<T, 64, 8, false>(p, stream);
+    if (p.s.N <= 128) return launch_k<T, 128, 8, false>(p, stream);
+    return launch_k<T, 256, 8, false>(p, stream);
 }
 
 }  // namespace ssd
