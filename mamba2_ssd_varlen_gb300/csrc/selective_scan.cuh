@@ -7,19 +7,28 @@
 //
 // Every (token, channel, state) costs an exponential and four fp32 operations on the
 // general pipe (two products, two multiply-adds); no part of it is a matrix product,
-// because the decay differs for every channel and state.  The kernel is bound by
-// instruction issue and those pipes, not by memory, so its shape is chosen to spend as
-// few other instructions as possible:
+// because the decay differs for every channel and state.  What bounds it: 32 (token,
+// channel)s of 16 states are 512 exponentials and 2048 fp32 operations, 64 cycles of an SM
+// quarter on either pipe (0.133 ms for 8 x 2048 tokens at D = 5120, above the 0.099 ms that
+// its bytes need), plus the step, the gate and their exchange.  Measured there: 0.458 ms,
+// instructions issued in 68 % of the cycles, shared-memory wavefronts at 64 %, fp32 pipe 47 %, special
+// functions 41 %; mixed prompts at D = 8192 1.246 ms, one of 131072 tokens at D = 4096
+// 4.40 ms.  A packed fp32 multiply-add with three different operands takes 3.2 cycles (the
+// register file's ports), two scalar ones 2.5, a packed product or sum 2.3 against 1.9: the
+// recurrence's multiply-adds are scalar, its first product and most of the rest packed.
+// The shape spends as few other instructions as it can:
 //   - a CTA walks the tokens of one request for 32 channels of one group; a lane holds
-//     two neighbouring channels as one packed fp32 pair (two multiply-adds an issue slot,
-//     and u, delta, z and y move as pairs) and NP / L of their states, L lanes a pair;
+//     two neighbouring channels (u, delta, z and y move as pairs) and NP / L of their
+//     states, L lanes a pair.  L = 4 for 16 states: two lanes leave too few warps to hide
+//     the special-function unit's latency (0.62 ms), eight exchange more (0.58 ms);
 //   - u, delta and z arrive by tiles of 16 tokens through asynchronous copies, two tiles
 //     ahead; B and C through registers, a tile ahead, laid out in shared memory as the
 //     (B, C) that a state needs, two states a 16-byte load;
 //   - softplus, u dt', the skip term and the gate are computed by the L lanes of a pair
 //     for different tokens, and exchanged through shared memory.  They, and the sums over
 //     the L lanes, belong to the blocks of TB tokens after and before the one whose
-//     recurrence runs beside them, so that their latency hides behind it.
+//     recurrence runs beside them, a stage between two of its tokens, so that their latency
+//     hides behind it (0.57 -> 0.51 ms).
 #pragma once
 
 #include "async_copy.cuh"
@@ -637,7 +646,7 @@ template <typename T>
 cudaError_t launch_selective_t(const SelParams &p, cudaStream_t stream) {
     if (p.s.N <= 8) return launch_k<T, 8, 4, true>(p, stream);
     // Sixteen states: four lanes a pair of channels where the GPU is full or requests are split, eight where up to two CTAs
-    // an SM leave a request's latency in the open (three short prompts 7.3 -> 6.7 us; 8 x 2048 tokens 472 -> 580 us).
+    // an SM leave a request's latency in the open (three short prompts: eight 6.7 us, four 7.3; 8 x 2048 tokens: four 0.47 ms, eight 0.58).
     if (p.s.N <= 16 && !p.seg && (int64_t)p.tiles * p.s.R <= 2 * 152) return launch_k<T, 16, 8, true>(p, stream);
     if (p.s.N <= 16) return launch_k<T, 16, 4, true>(p, stream);
     if (p.s.N <= 32) return launch_k<T, 32, 8, true>(p, stream);

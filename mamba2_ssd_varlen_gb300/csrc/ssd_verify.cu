@@ -14,7 +14,12 @@
 // the second digit the same way, so that no conversion instruction is needed.
 //
 // Bound by memory: one row of V probabilities for a window whose drafts were all accepted,
-// two after a rejection, and a few gathered entries.
+// two after a rejection, and a few gathered entries; a few windows by the chain of dependent
+// reads (window, drafts, their entries, the row, the chunk that holds the mark) and two
+// cluster barriers.  Measured at V = 131072, fp32: 256 windows of four 36.3 us (196 MB read:
+// 5.4 TB/s, 80 % of the copy rate), one window of eight 7 us.  Four CTAs of 256 threads an
+// SM, each lane with four 16-byte loads of each row in flight: three CTAs with eight 45 us,
+// a second wave of clusters 41 us.
 #include <cooperative_groups.h>
 
 #include "pdl.cuh"
