@@ -114,6 +114,28 @@ def test_long_request_with_block_checkpoints():
     scan(lengths=[3000, 700], D=33, N=20, block_size=256, num_computed=[100, 999], init_every=1)
 
 
+@pytest.mark.parametrize("layout", ["dense", "wide", "odd"])
+@pytest.mark.parametrize("lengths", [[0, 3000, 0, 5], [0, 0, 2100], [2049, 0, 1]])
+def test_long_and_empty_requests(lengths, layout):
+    scan(lengths=lengths, D=41, layout=layout, init_every=1, block_size=512, num_computed=[7] * len(lengths))
+
+
+def test_long_requests_with_bad_arguments():
+    kw = dict(lengths=[3000, 1200], D=40, device="cuda", init_every=1, block_size=256, num_computed=[0, 0])
+    clean = m.run_selective_scan(workloads.make_selective_problem(**kw))
+    assert m.ssd_varlen_selective_scan_workspace(clean.dims) > 0  # split over the time
+    for cu in ([0, 4300, 4200], [5, 3000, 4200], [0, 3000, 4100], [0, -7, 4200]):
+        prob = workloads.make_selective_problem(**kw)
+        prob["cu_seqlens"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        assert m.run_selective_scan(prob).status() & m.DEVERR["CU_SEQLENS"]
+    for field, bit in [("init_slots", "INIT_SLOT"), ("final_slots", "FINAL_SLOT"), ("block_table", "BLOCK_SLOT")]:
+        prob = workloads.make_selective_problem(**kw)
+        prob[field].view(-1)[-1 if field != "init_slots" else 0] = 5000
+        if field == "block_table":
+            prob[field][0, 10] = 5000
+        assert m.run_selective_scan(prob).status() == m.DEVERR[bit]
+
+
 def test_many_short_requests():
     scan(lengths=[(7 * i) % 23 for i in range(300)], D=40)
 
