@@ -55,11 +55,13 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 // Added to the argument of a decay's 2^x.  The unit's 2^x is low on average: by 5e-9 relative for x in (-2e-3, 0), by
 // 1e-8 to 3e-8 down to -0.2 (measured, 2^18 arguments a bin; its documented bound is 2^-22), and a state is a product of as
-// many decays as it remembers tokens, so a slow state would end up low by that many times as much.  1.2e-8 raises 2^x by
-// 8.3e-9, a quarter of a unit in the last place of a decay near 1: between the two, so that neither the slowest states
-// (mostly the initial one) nor the ordinary ones gather much.  Relative error of the final states against 64 bits, without
-// and with it: 13 ragged fp32 prompts 1.2e-6 and 7e-7, mixed bf16 prompts over 1e-6 and 8e-7; no time.
-constexpr float kDecayShift = 1.2e-8f;
+// many decays as it remembers tokens, so a slow state would end up low by that many times as much.  1.4e-8 raises 2^x by
+// 9.7e-9, a quarter of a unit in the last place of a decay near 1: between the two, so that neither the slowest states
+// (mostly the initial one) nor the ordinary ones gather much.  Relative error of the final states against 64 bits over
+// fixed and drawn prompts: 2e-7 to 1.2e-6 (13 ragged fp32 prompts: 1.2e-6 without it, 7e-7 with it), where exponentials
+// rounded correctly give 1e-7 to 2e-7; it costs no time, while a polynomial in place of the unit would cost the fp32 pipe
+// ten operations a state and token, more than twice what the recurrence itself takes there.
+constexpr float kDecayShift = 1.4e-8f;
 
 // softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|) in (0, 1], to a few units in the last
 // place for every v: log(1 + e) = 2 atanh(s) with s = e / (2 + e) <= 1/3, whose series in
