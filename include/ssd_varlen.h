@@ -505,10 +505,10 @@ int ssd_varlen_selective_step(const ssd_selective_dims *dims, const int32_t *cu_
  * first, bit for bit) goes to conv_pool[write_slots[t]] when that slot is >= 0.
  * io->read_slots is (R) and may be NULL (every window starts from zeros).  An
  * empty window reads and writes nothing.  dims and io as for ssd_varlen_conv1d,
- * with any D >= 1 and pointers aligned to their elements (16-byte aligned x, y
- * and pool with D a multiple of 16 bytes are read faster); sums and the SiLU are
- * fp32.  device_err receives CU_SEQLENS, INIT_SLOT, FINAL_SLOT.  One launch on
- * `stream`; allocates nothing. */
+ * with any D >= 1 and pointers aligned to their elements (x, y and pool aligned
+ * to four elements, weight to 16 bytes, and D a multiple of 4 are read faster);
+ * sums and the SiLU are fp32.  device_err receives CU_SEQLENS, INIT_SLOT,
+ * FINAL_SLOT.  One launch on `stream`; allocates nothing. */
 int ssd_varlen_conv1d_step(const ssd_conv_dims *dims, const int32_t *cu_seqlens, const ssd_conv_io *io,
                            cudaStream_t stream);
 

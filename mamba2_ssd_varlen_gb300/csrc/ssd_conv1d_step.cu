@@ -4,14 +4,15 @@
 //   y[t, c] = act(bias[c] + sum_k weight[c, k] xin[t - (W-1) + k, c])
 //   state after token t = xin[t - (W-2) .. t]
 //
-// Bound by memory and, at serving sizes, by the launch.  A thread owns kN neighbouring
-// channels, 16 bytes of a row of x: a slot's W-1 inputs a channel are then kN (W-1)
-// neighbouring elements, W-1 16-byte vectors, which move between their order in the slot
-// (channel by channel) and the window (input by input) in registers.  kN = 1 where rows,
-// slots or the width do not start on 16-byte boundaries.  A CTA takes several requests, one
-// after the other with the weights in registers, the next one's state on its way: as many as
-// leave one wave.  Measured at D = 5120, W = 4, bf16: 256 windows of one token 6.1 us (one
-// request a CTA: 9.1), of four 16.7 us (60 MB; 53 % of the copy rate).
+// Bound by memory and, at serving sizes, by the launch.  A thread owns four neighbouring
+// channels (one where the width or a pointer is off their boundary): a slot's W-1 inputs a
+// channel are then 4 (W-1) neighbouring elements, W-1 vectors, which move between their
+// order in the slot (channel by channel) and the window (input by input, held in fp32,
+// where every element is exact) by the naming of registers.  A CTA takes several requests,
+// one after the other with the weights in registers, the next one's state on its way: as
+// many as leave one wave.  Measured at D = 5120, W = 4, bf16: 256 windows of one token
+// 5.2 us (one request a CTA: 9.1), of four 15.8 us (60 MB; 56 % of the copy rate); eight
+// channels a thread take 126 to 157 registers, 6.3 and 16.8 us.
 #include <algorithm>
 
 #include "pdl.cuh"
@@ -31,33 +32,53 @@ struct ConvStepParams {
     ssd_conv_io io;
 };
 
-// kN raw elements, moved as one vector where kN elements are 16 bytes.
+// kN (1 or 4) neighbouring elements as they lie in memory, moved as one; in fp32 they are exact, so that the window can be
+// held there and handed back bit for bit.
 template <typename T, int kN>
 struct Raw {
-    T v[kN];
-    __device__ __forceinline__ void load(const T *p) {
-        if constexpr (kN * sizeof(T) == 16) {
-            const uint4 q = *reinterpret_cast<const uint4 *>(p);
-            memcpy(v, &q, 16);
-        } else {
-#pragma unroll
-            for (int e = 0; e < kN; ++e) v[e] = p[e];
-        }
+    static_assert(kN == 1, "one element");
+    T v;
+    __device__ __forceinline__ void load(const T *p) { v = *p; }
+    __device__ __forceinline__ void widen(float *x) const { x[0] = to_f32(v); }
+    __device__ __forceinline__ static void store(T *p, const float *x) { *p = from_f32<T>(x[0]); }
+    __device__ __forceinline__ static void store_exact(T *p, const float *x) {  // a rounding would rewrite a NaN's payload
+        if constexpr (sizeof(T) == 2)
+            *p = __ushort_as_bfloat16((unsigned short)(__float_as_uint(x[0]) >> 16));
+        else
+            *p = x[0];
     }
-    __device__ __forceinline__ void store(T *p) const {
-        if constexpr (kN * sizeof(T) == 16) {
-            uint4 q;
-            memcpy(&q, v, 16);
-            *reinterpret_cast<uint4 *>(p) = q;
-        } else {
-#pragma unroll
-            for (int e = 0; e < kN; ++e) p[e] = v[e];
-        }
+};
+template <>
+struct Raw<float, 4> {
+    float4 v;
+    __device__ __forceinline__ void load(const float *p) { v = *reinterpret_cast<const float4 *>(p); }
+    __device__ __forceinline__ void widen(float *x) const { x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w; }
+    __device__ __forceinline__ static void store(float *p, const float *x) {
+        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+    __device__ __forceinline__ static void store_exact(float *p, const float *x) { store(p, x); }
+};
+template <>
+struct Raw<__nv_bfloat16, 4> {
+    uint2 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void widen(float *x) const {
+        x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+        x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+    }
+    __device__ __forceinline__ static void store(__nv_bfloat16 *p, const float *x) {  // rounded
+        const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+        *reinterpret_cast<uint2 *>(p) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    }
+    __device__ __forceinline__ static void store_exact(__nv_bfloat16 *p, const float *x) {  // widened values: their upper halves
+        *reinterpret_cast<uint2 *>(p) = make_uint2(__byte_perm(__float_as_uint(x[0]), __float_as_uint(x[1]), 0x7632),
+                                                   __byte_perm(__float_as_uint(x[2]), __float_as_uint(x[3]), 0x7632));
     }
 };
 
 template <typename T, int W, int kN>
-__global__ void __launch_bounds__(kCsThreads) conv1d_step_kernel(const __grid_constant__ ConvStepParams p) {
+__global__ void __launch_bounds__(kCsThreads, 6) conv1d_step_kernel(const __grid_constant__ ConvStepParams p) {
     pdl_wait();
     const ssd_conv_io &io = p.io;
     const int lane = threadIdx.x & 31;
@@ -67,7 +88,7 @@ __global__ void __launch_bounds__(kCsThreads) conv1d_step_kernel(const __grid_co
     float w[kN * W], bias[kN];
 #pragma unroll
     for (int e = 0; e < kN; ++e) bias[e] = there && io.bias ? io.bias[c + e] : 0.f;
-    if constexpr (kN % 4 == 0) {
+    if constexpr (kN == 4) {
 #pragma unroll
         for (int e = 0; e < kN * W; e += 4)
             *reinterpret_cast<float4 *>(w + e) = there ? *reinterpret_cast<const float4 *>(io.weight + (size_t)c * W + e)
@@ -100,56 +121,50 @@ __global__ void __launch_bounds__(kCsThreads) conv1d_step_kernel(const __grid_co
         const int b = __shfl_sync(0xffffffffu, mb, q);
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
-            if (rs >= 0 && there) {
-                state[k].load(pool + rs * slot + off + k * kN);
-            } else {
-#pragma unroll
-                for (int e = 0; e < kN; ++e) state[k].v[e] = from_f32<T>(0.f);
-            }
+            state[k] = {};
+            if (rs >= 0 && there) state[k].load(pool + rs * slot + off + k * kN);
         }
         if (b > a && there) in.load(x + (size_t)a * p.D);
     };
     fetch(0);
     for (int q = 0; q < count; ++q) {
         const int a = __shfl_sync(0xffffffffu, ma, q), b = __shfl_sync(0xffffffffu, mb, q);
-        T win[W][kN];
+        float win[W][kN], flat[(W - 1) * kN];
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) state[k].widen(flat + k * kN);
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
 #pragma unroll
-            for (int e = 0; e < kN; ++e) win[k][e] = state[(e * (W - 1) + k) / kN].v[(e * (W - 1) + k) % kN];
-#pragma unroll
-        for (int e = 0; e < kN; ++e) win[W - 1][e] = in.v[e];
+            for (int e = 0; e < kN; ++e) win[k][e] = flat[e * (W - 1) + k];
+        in.widen(win[W - 1]);
         if (q + 1 < count) fetch(q + 1);  // on its way while this window is computed
         for (int t = a; t < b; ++t) {
             const int ws = io.write_slots ? io.write_slots[t] : -1;
-            Raw<T, kN> ahead, out;
+            Raw<T, kN> ahead = {};
             if (t + 1 < b && there) ahead.load(x + (size_t)(t + 1) * p.D);
+            float out[kN];
 #pragma unroll
             for (int e = 0; e < kN; ++e) {
                 float v = bias[e];
 #pragma unroll
-                for (int k = 0; k < W; ++k) v = fmaf(w[e * W + k], to_f32(win[k][e]), v);
-                out.v[e] = from_f32<T>(p.silu ? silu_sfu(v) : v);
+                for (int k = 0; k < W; ++k) v = fmaf(w[e * W + k], win[k][e], v);
+                out[e] = p.silu ? silu_sfu(v) : v;
             }
-            if (there) out.store(y + (size_t)t * p.D);
+            if (there) Raw<T, kN>::store(y + (size_t)t * p.D, out);
             if (ws >= p.num_slots) {
                 if (c == 0) atomicOr(io.device_err, SSD_DEVERR_FINAL_SLOT);
             } else if (ws >= 0 && there) {
 #pragma unroll
-                for (int k = 0; k < W - 1; ++k) {
-                    Raw<T, kN> s;
+                for (int i = 0; i < (W - 1) * kN; ++i) flat[i] = win[i % (W - 1) + 1][i / (W - 1)];
 #pragma unroll
-                    for (int e = 0; e < kN; ++e)
-                        s.v[e] = win[(k * kN + e) % (W - 1) + 1][(k * kN + e) / (W - 1)];
-                    s.store(pool + ws * slot + off + k * kN);
-                }
+                for (int k = 0; k < W - 1; ++k)
+                    Raw<T, kN>::store_exact(pool + ws * slot + off + k * kN, flat + k * kN);
             }
 #pragma unroll
-            for (int e = 0; e < kN; ++e) {
+            for (int k = 0; k < W - 1; ++k)
 #pragma unroll
-                for (int k = 0; k < W - 1; ++k) win[k][e] = win[k + 1][e];
-                win[W - 1][e] = ahead.v[e];
-            }
+                for (int e = 0; e < kN; ++e) win[k][e] = win[k + 1][e];
+            ahead.widen(win[W - 1]);
         }
     }
 }
@@ -170,15 +185,15 @@ cudaError_t launch_cs_n(ConvStepParams &p, cudaStream_t stream) {
 
 template <typename T, int W>
 cudaError_t launch_cs_w(ConvStepParams &p, bool vec, cudaStream_t stream) {
-    return vec ? launch_cs_n<T, W, 16 / sizeof(T)>(p, stream) : launch_cs_n<T, W, 1>(p, stream);
+    return vec ? launch_cs_n<T, W, 4>(p, stream) : launch_cs_n<T, W, 1>(p, stream);
 }
 
 bool aligned_to(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 template <typename T>
 cudaError_t launch_cs(ConvStepParams &p, int W, cudaStream_t stream) {
-    const bool vec = p.D % (16 / (int)sizeof(T)) == 0 && aligned_to(p.io.x, 16) && aligned_to(p.io.y, 16) &&
-                     aligned_to(p.io.conv_pool, 16) && aligned_to(p.io.weight, 16);
+    const bool vec = p.D % 4 == 0 && aligned_to(p.io.x, 4 * sizeof(T)) && aligned_to(p.io.y, 4 * sizeof(T)) &&
+                     aligned_to(p.io.conv_pool, 4 * sizeof(T)) && aligned_to(p.io.weight, 16);
     switch (W) {
         case 2: return launch_cs_w<T, 2>(p, vec, stream);
         case 3: return launch_cs_w<T, 3>(p, vec, stream);

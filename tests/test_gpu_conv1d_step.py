@@ -102,3 +102,46 @@ def test_without_slots_with_bad_slots_and_on_another_stream(D):
         assert m.run_conv1d_step(prob).status() & m.DEVERR["CU_SEQLENS"]
     prob = workloads.make_conv_step_problem([0, 0], D=D, device="cuda")
     assert m.run_conv1d_step(prob).status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("D", [64, 33])
+def test_states_keep_every_bit_pattern(D, dtype):
+    """Negative and payload-carrying NaN, infinities, zeros of both signs and subnormals pass through a slot."""
+    prob = workloads.make_conv_step_problem(windows=[1, 3, 2], D=D, W=4, dtype=dtype, seed=2, device="cuda")
+    words = [0x7FC0, 0xFFC0, 0x7F81, 0xFFFF, 0x7F80, 0xFF80, 0x0000, 0x8000, 0x0001, 0x8001, 0x3F80]
+    words = [w - 0x10000 if w >= 0x8000 else w for w in words]
+    for name in ("x", "conv_pool"):
+        flat = prob[name].view(torch.int16).reshape(-1)
+        fill = torch.tensor(words, dtype=torch.int16, device="cuda").repeat(flat.numel() // len(words) + 1)
+        flat.copy_(fill[:flat.numel()])
+    before = prob["conv_pool"].clone()
+    call = m.run_conv1d_step(prob)
+    torch.cuda.synchronize()
+    assert call.status() == 0
+    cu, read, write = (prob[k].tolist() for k in ("cu_seqlens", "read_slots", "write_slots"))
+    want = before.clone()
+    for i in range(prob["R"]):
+        seq = before[read[i]] if read[i] >= 0 else torch.zeros_like(before[0])
+        for t in range(cu[i], cu[i + 1]):
+            seq = torch.cat([seq, prob["x"][t][:, None]], 1)[:, -3:]
+            if write[t] >= 0:
+                want[write[t]] = seq
+    assert torch.equal(prob["conv_pool"].view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("moved", ["x", "conv_pool", "weight"])
+def test_pointers_off_the_vector_boundary(moved, dtype):
+    """The same problem with one tensor an element further on gives the same bits."""
+    def problem():
+        return workloads.make_conv_step_problem(windows=[1, 4, 2], D=64, W=4, dtype=dtype, seed=8, device="cuda")
+    plain, off = problem(), problem()
+    room = torch.empty(off[moved].numel() + 1, dtype=off[moved].dtype, device="cuda")
+    view = room[1:].view(off[moved].shape)
+    view.copy_(off[moved])
+    off[moved] = view
+    a, b = m.run_conv1d_step(plain), m.run_conv1d_step(off)
+    torch.cuda.synchronize()
+    assert a.status() == 0 and b.status() == 0
+    assert torch.equal(a.y, b.y) and torch.equal(plain["conv_pool"], off["conv_pool"])
