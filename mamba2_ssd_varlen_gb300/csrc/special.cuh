@@ -58,7 +58,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // many decays as it remembers tokens, so a slow state would end up low by that many times as much.  1.4e-8 raises 2^x by
 // 9.7e-9, a quarter of a unit in the last place of a decay near 1: between the two, so that neither the slowest states
 // (mostly the initial one) nor the ordinary ones gather much.  Relative error of the final states against 64 bits over
-// fixed and drawn prompts: 2e-7 to 1.2e-6 (13 ragged fp32 prompts: 1.2e-6 without it, 7e-7 with it), where exponentials
+// fixed and drawn prompts: 2e-7 to 1.4e-6 (13 ragged fp32 prompts: 1.2e-6 without it, 7e-7 with it), where exponentials
 // rounded correctly give 1e-7 to 2e-7; it costs no time, while a polynomial in place of the unit would cost the fp32 pipe
 // ten operations a state and token, more than twice what the recurrence itself takes there.
 constexpr float kDecayShift = 1.4e-8f;
